@@ -43,6 +43,10 @@ class _HaloBox(ctypes.Structure):
                 ("msg_offset", ctypes.c_int64)]
 
 
+class _Tokens(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
 class _GnLayout(ctypes.Structure):
     _fields_ = [("partials_offset", ctypes.c_size_t), ("stats_offset", ctypes.c_size_t),
                 ("scales_offset", ctypes.c_size_t), ("ymax_offset", ctypes.c_size_t),
@@ -72,6 +76,7 @@ def _load() -> ctypes.CDLL:
         raise ImportError(f"two HIP runtimes are loaded ({runtimes}); import torch before any other HIP library")
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     PP = ctypes.POINTER(ctypes.c_void_p)
+    PI32, PT = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(_Tokens)
     sig = {
         "st_version": (ctypes.c_char_p, []),
         "st_last_error": (ctypes.c_char_p, []),
@@ -115,6 +120,18 @@ def _load() -> ctypes.CDLL:
         "st_groupnorm_combine_apply": (I32, [P, PP, I32, ctypes.c_float, P, P, PP, P, SZ, P]),
         "st_groupnorm_backward_workspace_bytes": (SZ, [P, I32]),
         "st_groupnorm_backward": (I32, [P, PP, PP, P, P, I32, P, P, SZ, P, PP, P, P, P, SZ, P]),
+        "st_layernorm_sharded": (I32, [P, PP, P, P, ctypes.c_float, P, PP, P, P]),
+        "st_layernorm_backward_workspace_bytes": (SZ, [P]),
+        "st_layernorm_backward": (I32, [P, PP, P, PP, P, P, P, PP, P, P, P, SZ, P]),
+        "st_plan_positions": (I32, [P, PP, P]),
+        "st_rope_axes": (I32, [P, I32, I64, I64, I64, I32, I32, I32, P, I32, PI32, ctypes.c_double, I32, I32, P, I32,
+                               I64, I64, P]),
+        "st_plan_sequences": (I32, [I32, PI32, PI32, I32, I32, I32, I32, I32, ctypes.POINTER(P)]),
+        "st_seqs_destroy": (I32, [P]),
+        "st_seqs_upload": (I32, [P, P]),
+        "st_attention_workspace_bytes": (SZ, [P, I32]),
+        "st_attention_packed": (I32, [P, PT, PT, PT, ctypes.c_float, PT, P, P, SZ, P]),
+        "st_attention_packed_backward": (I32, [P, PT, PT, PT, PT, P, PT, ctypes.c_float, PT, PT, PT, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -148,6 +165,8 @@ class Plan:
         self.ndim, self.batch, self.channels, self.dtype = ndim, batch, channels, dtype
         self.shards = tuple(tuple(s) for s in shards)
         self.halo = tuple(halo)
+        self._bytes = None
+        self._cells = None
 
     @property
     def handle(self) -> ctypes.c_void_p:
@@ -261,7 +280,9 @@ def _ptr_array(tensors, what: str, sizes: List[int]):
 
 
 def _shard_bytes(plan: Plan) -> List[int]:
-    return [plan.shard_info(i)["bytes"] for i in range(plan.num_shards)]
+    if plan._bytes is None:                  # fixed for a plan's life
+        plan._bytes = [plan.shard_info(i)["bytes"] for i in range(plan.num_shards)]
+    return plan._bytes
 
 
 def st_halo_pack(plan: Plan, shard_bufs, msg, stream=None) -> None:
@@ -589,3 +610,194 @@ __all__ = [
     "st_pool_sharded", "st_plan_strided", "st_conv_strided_sharded", "st_plan_transposed",
     "st_conv_transposed_sharded",
 ]
+
+
+# ------------------------------------------------------------ token operators
+
+def _cells(plan: Plan) -> List[int]:
+    """Interior cells of every shard."""
+    if plan._cells is None:
+        out = []
+        for i in range(plan.num_shards):
+            n = plan.batch
+            for e in plan.shard_info(i)["extent"]:
+                n *= e
+            out.append(n)
+        plan._cells = out
+    return plan._cells
+
+
+def st_layernorm_sharded(x_plan: Plan, x_bufs, gamma, beta, eps: float, y_plan: Plan, y_bufs, stats=None,
+                         stream=None) -> None:
+    """Layer norm over the channels of every cell; stats: 2 floats per cell
+    (mean, 1 / sqrt(var + eps)), shard by shard, or None."""
+    xs = _ptr_array(x_bufs, "st_layernorm_sharded x", _shard_bytes(x_plan))
+    ys = _ptr_array(y_bufs, "st_layernorm_sharded y", _shard_bytes(y_plan))
+    g = _dev_ptr(gamma, "gamma", 4 * x_plan.channels)
+    b = _dev_ptr(beta, "beta", 4 * x_plan.channels)
+    st = _dev_ptr(stats, "stats", 8 * sum(_cells(x_plan)))
+    _check(lib.st_layernorm_sharded(x_plan.handle, xs, g, b, float(eps), y_plan.handle, ys, st, _stream(stream)),
+           "st_layernorm_sharded")
+
+
+def st_layernorm_backward_workspace_bytes(x_plan: Plan) -> int:
+    return int(lib.st_layernorm_backward_workspace_bytes(x_plan.handle))
+
+
+def st_layernorm_backward(x_plan: Plan, x_bufs, dy_plan: Plan, dy_bufs, gamma, stats, dx_plan: Plan, dx_bufs, dgamma,
+                          dbeta, workspace, stream=None) -> None:
+    """stats: as st_layernorm_sharded wrote them; dgamma, dbeta: C floats or None."""
+    xs = _ptr_array(x_bufs, "st_layernorm_backward x", _shard_bytes(x_plan))
+    dys = _ptr_array(dy_bufs, "st_layernorm_backward dy", _shard_bytes(dy_plan))
+    dxs = _ptr_array(dx_bufs, "st_layernorm_backward dx", _shard_bytes(dx_plan))
+    c = 4 * x_plan.channels
+    ws, nb = _ws(workspace)
+    _check(lib.st_layernorm_backward(x_plan.handle, xs, dy_plan.handle, dys, _dev_ptr(gamma, "gamma", c),
+                                     _dev_ptr(stats, "stats", 8 * sum(_cells(x_plan))), dx_plan.handle, dxs,
+                                     _dev_ptr(dgamma, "dgamma", c), _dev_ptr(dbeta, "dbeta", c), ws, nb,
+                                     _stream(stream)), "st_layernorm_backward")
+
+
+def st_plan_positions(plan: Plan, pos_bufs, stream=None) -> None:
+    """Global int32 grid positions [N][extent...][ndim] of every shard's cells."""
+    ps = _ptr_array(pos_bufs, "st_plan_positions", [4 * plan.ndim * n for n in _cells(plan)])
+    _check(lib.st_plan_positions(plan.handle, ps, _stream(stream)), "st_plan_positions")
+
+
+def _float_dtype(t, what: str) -> int:
+    """ST_F32 or ST_BF16 of a tensor (bf16 also as int16 bit patterns)."""
+    torch = _torch()
+    if t.dtype == torch.float32:
+        return ST_F32
+    if t.dtype in (torch.bfloat16, torch.int16):
+        return ST_BF16
+    raise ShardConvError(1, f"{what}: expected float32 or bfloat16, got {t.dtype}")
+
+
+def _rows3(t, what: str):
+    """Checks of a [tokens, heads, head_dim] tensor with contiguous channels."""
+    if not getattr(t, "is_cuda", False):
+        raise ShardConvError(1, f"{what}: expected a GPU tensor (no CPU fallback exists)")
+    if t.dim() != 3:
+        raise ShardConvError(2, f"{what}: expected [tokens, heads, head_dim], got {tuple(t.shape)}")
+    if t.numel() and t.shape[2] > 1 and t.stride(2) != 1:
+        raise ShardConvError(2, f"{what}: channels must be contiguous")
+
+
+_PAIRS = {"halves": 0, "adjacent": 1}
+
+
+def st_rope_axes(x, positions, axis_dims: Sequence[int], out, rotated_heads: Optional[int] = None,
+                 base: float = 10000.0, pairs: str = "halves", inverse: bool = False, stream=None) -> None:
+    """Rotary positions with one section of channels per axis.
+
+    x, out: [tokens, heads, head_dim], float32 or bfloat16 each, any token and
+    head strides; out may be x.  positions: int32 [tokens, axes].
+    rotated_heads: heads that turn (default all), the others are copied.
+    """
+    _rows3(x, "st_rope_axes x")
+    _rows3(out, "st_rope_axes out")
+    tokens, heads, dim = x.shape
+    if tuple(out.shape) != (tokens, heads, dim):
+        raise ShardConvError(2, f"st_rope_axes: out is {tuple(out.shape)}, x is {tuple(x.shape)}")
+    if pairs not in _PAIRS:
+        raise ShardConvError(1, f"st_rope_axes: unknown pairing {pairs!r}")
+    n = len(axis_dims)
+    if positions.dtype != _torch().int32:
+        raise ShardConvError(1, "st_rope_axes: positions must be int32")
+    pos = _dev_ptr(positions, "positions", 4 * tokens * n)
+    dims = (ctypes.c_int32 * max(1, n))(*axis_dims)
+    _check(lib.st_rope_axes(x.data_ptr(), _float_dtype(x, "st_rope_axes x"), x.stride(0), x.stride(1), tokens, heads,
+                            heads if rotated_heads is None else rotated_heads, dim, pos, n, dims, float(base),
+                            _PAIRS[pairs], int(bool(inverse)), out.data_ptr(), _float_dtype(out, "st_rope_axes out"),
+                            out.stride(0), out.stride(1), _stream(stream)), "st_rope_axes")
+
+
+class Sequences:
+    """Owns an st_seqs*: the work plan of attention over packed sequences."""
+
+    def __init__(self, handle: int, q_lens, k_lens, heads: int, kv_heads: int, head_dim: int, dtype: int, causal: bool):
+        self._h = ctypes.c_void_p(handle)
+        self.total_q, self.total_k = sum(q_lens), sum(k_lens)
+        self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
+        self.dtype, self.causal = dtype, causal
+
+    @property
+    def handle(self) -> ctypes.c_void_p:
+        if not self._h:
+            raise ShardConvError(1, "sequences already destroyed")
+        return self._h
+
+    def destroy(self) -> None:
+        if self._h:
+            _check(lib.st_seqs_destroy(self._h), "st_seqs_destroy")
+            self._h = ctypes.c_void_p(0)
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+    def upload(self, stream=None) -> None:
+        """Put the work tables on the current device now (needed before a graph
+        capture that contains the first attention call)."""
+        _check(lib.st_seqs_upload(self.handle, _stream(stream)), "st_seqs_upload")
+
+
+def st_plan_sequences(q_lens: Sequence[int], k_lens: Optional[Sequence[int]], heads: int, kv_heads: int, head_dim: int,
+                      dtype, causal: bool) -> Sequences:
+    """Plan of attention over packed sequences of q_lens queries and k_lens
+    (None: q_lens) keys; dtype 'f32'/'bf16' or 0/1."""
+    q = list(q_lens)
+    k = q if k_lens is None else list(k_lens)
+    if len(q) != len(k):
+        raise ShardConvError(2, f"st_plan_sequences: {len(q)} query lengths and {len(k)} key lengths")
+    if any(n < 0 or n >= 1 << 31 for n in q + k):
+        raise ShardConvError(1, "st_plan_sequences: a length is negative or past 2^31")
+    dt = DTYPES.get(dtype, dtype)
+    qa = (ctypes.c_int32 * max(1, len(q)))(*q)
+    ka = (ctypes.c_int32 * max(1, len(k)))(*k)
+    out = ctypes.c_void_p()
+    _check(lib.st_plan_sequences(len(q), qa, ka, heads, kv_heads, head_dim, dt, int(bool(causal)), ctypes.byref(out)),
+           "st_plan_sequences")
+    return Sequences(out.value, q, k, heads, kv_heads, head_dim, dt, bool(causal))
+
+
+def st_attention_workspace_bytes(seqs: Sequences, backward: bool = False) -> int:
+    return int(lib.st_attention_workspace_bytes(seqs.handle, int(bool(backward))))
+
+
+def _tokens(t, what: str, seqs: Sequences, keys: bool) -> _Tokens:
+    _rows3(t, what)
+    want = (seqs.total_k if keys else seqs.total_q, seqs.kv_heads if keys else seqs.heads, seqs.head_dim)
+    if tuple(t.shape) != want:
+        raise ShardConvError(2, f"{what}: expected {want}, got {tuple(t.shape)}")
+    if _float_dtype(t, what) != seqs.dtype:
+        raise ShardConvError(1, f"{what}: dtype {t.dtype} is not the plan's")
+    return _Tokens(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def st_attention_packed(seqs: Sequences, q, k, v, scale: float, out, lse=None, workspace=None, stream=None) -> None:
+    """q, out: [total queries, heads, head_dim]; k, v: [total keys, kv_heads,
+    head_dim]; any strides that are multiples of 16 bytes; lse: float32
+    [total queries, heads] or None."""
+    what = "st_attention_packed"
+    args = [_tokens(t, f"{what} {n}", seqs, n in "kv") for n, t in (("q", q), ("k", k), ("v", v), ("out", out))]
+    l = _dev_ptr(lse, f"{what} lse", 4 * seqs.total_q * seqs.heads)
+    ws, nb = _ws(workspace)
+    _check(lib.st_attention_packed(seqs.handle, args[0], args[1], args[2], float(scale), args[3], l, ws, nb,
+                                   _stream(stream)), what)
+
+
+def st_attention_packed_backward(seqs: Sequences, q, k, v, out, lse, dout, scale: float, dq, dk, dv, workspace,
+                                 stream=None) -> None:
+    """dq, dk, dv of st_attention_packed; out and lse as it wrote them."""
+    what = "st_attention_packed_backward"
+    args = [_tokens(t, f"{what} {n}", seqs, keys) for n, t, keys in
+            (("q", q, False), ("k", k, True), ("v", v, True), ("out", out, False), ("dout", dout, False),
+             ("dq", dq, False), ("dk", dk, True), ("dv", dv, True))]
+    l = _dev_ptr(lse, f"{what} lse", 4 * seqs.total_q * seqs.heads)
+    ws, nb = _ws(workspace)
+    _check(lib.st_attention_packed_backward(seqs.handle, args[0], args[1], args[2], args[3], l, args[4], float(scale),
+                                            args[5], args[6], args[7], ws, nb, _stream(stream)), what)

@@ -16,7 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libshardconv.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
-SOURCES = ["plan.cpp", "halo.hip", "conv.hip", "wgrad.hip", "groupnorm.hip", "pool.hip", "strided.hip"]
+SOURCES = ["plan.cpp", "halo.hip", "conv.hip", "wgrad.hip", "groupnorm.hip", "pool.hip", "strided.hip",
+           "layernorm.hip", "rope.hip", "sequences.cpp", "attention.hip", "attention_bwd.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

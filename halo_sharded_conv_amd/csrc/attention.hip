@@ -1,0 +1,426 @@
+// Attention over packed sequences: forward.
+//
+//   out = softmax(scale * q k^T) v,   lse = log sum exp(scale * q k^T)
+// per sequence and head, in one pass over the keys: with the running maximum m
+// and denominator l of a row, a tile of scores s adds p = exp(s - m), and where
+// m grows, l and the output so far are scaled by exp(m_old - m_new).
+//
+// The products run transposed: S^T = K Q^T, then O^T += V^T P^T.  A lane then
+// holds one row (query) of the scores and of the output for its whole life, so
+// the maximum and the sum of a row need one exchange between the wave's
+// halves per tile and none inside a product, and the scores go from the first
+// product to the second in registers.  See attention.h for the LDS tiles.
+//
+// Rows are (token, head of the group) pairs, so heads that share keys share
+// the tiles of K and V, and a single query token of a grouped head still fills
+// the rows of a tile.
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "attention.h"
+
+namespace st {
+namespace {
+
+// m grows only where a tile exceeds it by more than this (in powers of two):
+// p stays below 2^8, and most tiles then scale nothing
+constexpr float kSlack = 8.f;
+
+// The parts of a V fragment that a matrix product must not see next to a zero
+// weight: 0 * inf and 0 * NaN are NaN, but a masked key has no weight at all.
+template <class T> struct Special;
+template <> struct Special<BF16> {
+  static __device__ __forceinline__ bool any(bf16x8 v) {
+    const u32x4_t w = __builtin_bit_cast(u32x4_t, v);
+    bool f = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f = f || (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
+    return f;
+  }
+  // kind 0: the finite values, 1: one where NaN, 2: one where +inf, 3: one where -inf
+  static __device__ __forceinline__ bf16x8 pick(bf16x8 v, int kind) {
+    typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+    const u16x8 w = __builtin_bit_cast(u16x8, v);
+    u16x8 o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint16_t b = w[i];
+      const bool inf = (b & 0x7FFF) == 0x7F80, nan = (b & 0x7FFF) > 0x7F80;
+      const bool one = kind == 1 ? nan : kind == 2 ? inf && !(b >> 15) : inf && (b >> 15);
+      o[i] = kind == 0 ? (inf || nan ? 0 : b) : (one ? 0x3F80 : 0);
+    }
+    return __builtin_bit_cast(bf16x8, o);
+  }
+};
+template <> struct Special<F32> {
+  static __device__ __forceinline__ bool any(f32x8 v) {
+    bool f = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f = f || (__float_as_uint(v[i]) & 0x7F800000u) == 0x7F800000u;
+    return f;
+  }
+  static __device__ __forceinline__ f32x8 pick(f32x8 v, int kind) {
+    f32x8 o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t b = __float_as_uint(v[i]);
+      const bool inf = (b & 0x7FFFFFFFu) == 0x7F800000u, nan = (b & 0x7FFFFFFFu) > 0x7F800000u;
+      const bool one = kind == 1 ? nan : kind == 2 ? inf && !(b >> 31) : inf && (b >> 31);
+      o[i] = kind == 0 ? (inf || nan ? 0.f : v[i]) : (one ? 1.f : 0.f);
+    }
+    return o;
+  }
+};
+
+template <class T, int DP, int KT, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void attn_forward(const AttnArgs a) {
+  using M = Mma<T>;
+  using Tl = Tile<T, DP, KT, NW>;
+  constexpr int KB = KT / 32, SR = Tl::SR, DB = Tl::DB, NI = Tl::NI;
+  __shared__ __attribute__((aligned(1024))) char k0s[Tl::BYTES];
+  __shared__ __attribute__((aligned(1024))) char v0s[Tl::BYTES];
+  __shared__ __attribute__((aligned(1024))) char k1s[Tl::BYTES];
+  __shared__ __attribute__((aligned(1024))) char v1s[Tl::BYTES];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, l32 = lane & 31;
+  const int kvh = blockIdx.x % a.kv_heads;
+  const AttnItem it = a.items[blockIdx.x / a.kv_heads];
+
+  const int row0 = it.at + wave * 32;                   // the wave's first row
+  const int row = row0 + l32;
+  const int token = (int)quo(row, a.by_group), head = kvh * a.group + row - token * a.group;
+  const bool live = token < it.lq;
+  const int off = it.lk - it.lq;                        // causal: token i sees keys <= i + off
+  // keys below `limit` are seen by this lane's row
+  const int limit = a.causal ? min(it.lk, token + off + 1) : it.lk;
+  const int wave_token = (int)quo(row0, a.by_group);    // lowest limit of the wave
+  const int wave_limit = a.causal ? min(it.lk, wave_token + off + 1) : it.lk;
+  const int wave_last = a.causal ? min(it.lk, (int)quo(row0 + 31, a.by_group) + off + 1) : it.lk;
+
+  typename M::Row qf[SR];
+  {
+    const char* p = a.q.p + (int64_t)(it.q0 + token) * a.q.t + (int64_t)head * a.q.h;
+#pragma unroll
+    for (int s = 0; s < SR; ++s) {
+      const int byte = (2 * s + half) * 16;
+      qf[s] = live && byte < a.dim * T::kSize ? *reinterpret_cast<const typename M::Row*>(p + byte) : typename M::Row{};
+    }
+  }
+  // this lane's transfers: byte offsets within a tile of K and of V
+  uint32_t koff[NI], voff[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int r = Tl::dma_row(wave, lane, i), b = Tl::dma_byte(wave, lane, i);
+    const bool in = b < a.dim * T::kSize;
+    koff[i] = in ? (uint32_t)(r * (int)a.k.t + b) : kOobOffset;
+    voff[i] = in ? (uint32_t)(r * (int)a.v.t + b) : kOobOffset;
+  }
+  const char* kb = a.k.p + (int64_t)it.k0 * a.k.t + (int64_t)kvh * a.k.h;
+  const char* vb = a.v.p + (int64_t)it.k0 * a.v.t + (int64_t)kvh * a.v.h;
+
+  f32x16 o[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) o[d] = f32x16{};
+  float m = -INFINITY, l = 0.f;
+
+  auto fetch = [&](char* ks, char* vs, int j0) __attribute__((always_inline)) {
+    const int64_t left = min(KT, it.hi - j0);            // rows past the range read zeros
+    const auto rk = attn_rsrc(kb + (int64_t)j0 * a.k.t, left * a.k.t);
+    const auto rv = attn_rsrc(vb + (int64_t)j0 * a.v.t, left * a.v.t);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const uint32_t at = koff[i];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_void)Tl::dma_dst(ks, wave, i), 16, at, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const uint32_t at = voff[i];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_void)Tl::dma_dst(vs, wave, i), 16, at, 0, 0, 0);
+    }
+  };
+
+  auto step = [&](const char* ks, const char* vs, char* kn, char* vn, int j0) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);                 // vmcnt(0): this tile is in LDS
+    __syncthreads();                                    // ... for every wave; the other tile is free
+    if (j0 + KT < it.hi) fetch(kn, vn, j0 + KT);
+    if (j0 >= wave_last) return;                        // (uniform) nothing here is seen by these rows
+    f32x16 s[KB];
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+      s[b] = f32x16{};
+#pragma unroll
+      for (int c = 0; c < SR; ++c) s[b] = M::rows(Tl::row(ks, b, c, lane), qf[c], s[b]);
+    }
+    const bool masked = j0 + KT > wave_limit;
+    if (masked) {
+      const int lim = limit - j0 - 4 * half;
+#pragma unroll
+      for (int b = 0; b < KB; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (32 * b + 8 * (r / 4) + r % 4 >= lim) s[b][r] = -INFINITY;
+    }
+    float mx = s[0][0];
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[b][r]);
+    mx = half_max(mx) * a.scale_log2;
+    if (__any(mx > m + kSlack)) {
+      const float mn = mx > m + kSlack ? mx : m;        // row by row: a row's bits are its own
+      const float f = mn == m ? 1.f : exp2_hw(m - mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[d][r] *= f;
+    }
+    const float ms = m == -INFINITY ? 0.f : m;          // no key seen so far: p = 0
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[b][r] = exp2_hw(fmaf(s[b][r], a.scale_log2, -ms));
+        l += s[b][r];
+      }
+    if (masked && a.causal) {
+      // a later key's NaN or infinity has no part in an earlier row
+      bool sp = false;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) sp |= Special<T>::any(Tl::col(vs, b, t, d, lane));
+      if (__any(sp)) {
+        const int lim = limit - j0 - 4 * half;
+        for (int d = 0; d < DB; ++d) {
+          f32x16 cn = f32x16{}, cp = f32x16{}, cm = f32x16{}, od = o[0];
+#pragma unroll
+          for (int e = 1; e < DB; ++e) od = d == e ? o[e] : od;
+#pragma unroll
+          for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              f32x16 seen, pos, zero;
+#pragma unroll
+              for (int r = 0; r < 16; ++r) {
+                const bool vis = 32 * b + 8 * (r / 4) + r % 4 < lim;
+                seen[r] = vis ? 1.f : 0.f;
+                pos[r] = vis && s[b][r] > 0.f ? 1.f : 0.f;
+                zero[r] = vis && !(s[b][r] > 0.f) ? 1.f : 0.f;
+              }
+              const typename M::Col w = Tl::col(vs, b, t, d, lane);
+              const typename M::Col pinf = Special<T>::pick(w, 2), minf = Special<T>::pick(w, 3);
+              od = M::cols(Special<T>::pick(w, 0), M::regs(s[b], t), od);
+              cn = M::cols(Special<T>::pick(w, 1), M::regs(seen, t), cn);
+              cn = M::cols(pinf, M::regs(zero, t), cn);
+              cn = M::cols(minf, M::regs(zero, t), cn);
+              cp = M::cols(pinf, M::regs(pos, t), cp);
+              cm = M::cols(minf, M::regs(pos, t), cm);
+            }
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            if (cp[r] > 0.f) od[r] += INFINITY;
+            if (cm[r] > 0.f) od[r] -= INFINITY;
+            if (cn[r] > 0.f) od[r] = NAN;
+          }
+#pragma unroll
+          for (int e = 0; e < DB; ++e)
+            if (d == e) o[e] = od;
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const typename M::Col p = M::regs(s[b], t);
+#pragma unroll
+        for (int d = 0; d < DB; ++d) o[d] = M::cols(Tl::col(vs, b, t, d, lane), p, o[d]);
+      }
+  };
+
+  if (it.lo < it.hi) {
+    fetch(k0s, v0s, it.lo);
+    for (int j = it.lo; j < it.hi; j += 2 * KT) {
+      step(k0s, v0s, k1s, v1s, j);
+      if (j + KT < it.hi) step(k1s, v1s, k0s, v0s, j + KT);
+    }
+  }
+
+  l = half_sum(l);
+  const float inv = l == 0.f ? 0.f : 1.f / l;           // a row that sees no key: zeros
+  if (it.part >= 0) {
+    const int64_t slot = ((int64_t)it.part * a.kv_heads + kvh) * (32 * NW) + wave * 32 + l32;
+    if (half == 0) a.part2[slot] = l == 0.f ? -INFINITY : m + log2f(l);
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+      store_block<F32>(reinterpret_cast<char*>(a.part + slot * DP), o[d], inv, d, DP, lane);
+    return;
+  }
+  if (!live) return;
+  if (half == 0 && a.lse)
+    a.lse[(int64_t)(it.q0 + token) * a.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  char* po = a.out.p + (int64_t)(it.q0 + token) * a.out.t + (int64_t)head * a.out.h;
+#pragma unroll
+  for (int d = 0; d < DB; ++d) store_block<T>(po, o[d], inv, d, a.dim, lane);
+}
+
+// Joins the parts of a tile whose keys were split: each part is a softmax of its
+// own with log2 of its denominator, so the whole is their sum weighted by
+// 2^(part - max).  A thread takes four channels of one row.
+template <class T, int DP>
+__global__ __launch_bounds__(256) void attn_join(const AttnArgs a, int tile) {
+  const int kvh = blockIdx.x % a.kv_heads;
+  const AttnJoin j = a.joins[blockIdx.x / a.kv_heads];
+  for (int i = threadIdx.x; i < tile * (DP / 4); i += 256) {
+    const int r = i / (DP / 4), c = i % (DP / 4) * 4;
+    const int row = j.at + r, token = (int)quo(row, a.by_group), head = kvh * a.group + row - token * a.group;
+    if (token >= j.lq || c >= a.dim) continue;
+    float m = -INFINITY;
+    for (int p = 0; p < j.count; ++p)
+      m = fmaxf(m, a.part2[((int64_t)(j.first + p) * a.kv_heads + kvh) * tile + r]);
+    const float ms = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    f32x4_t o = f32x4_t{};
+#pragma unroll 4
+    for (int p = 0; p < j.count; ++p) {
+      const int64_t slot = ((int64_t)(j.first + p) * a.kv_heads + kvh) * tile + r;
+      const float w = exp2_hw(a.part2[slot] - ms);
+      l += w;
+      o += w * *reinterpret_cast<const f32x4_t*>(a.part + slot * DP + c);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t tok = j.q0 + token;
+    if (c == 0 && a.lse) a.lse[tok * a.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    const float x[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+    store_vec<T, 4>(a.out.p + tok * a.out.t + (int64_t)head * a.out.h + c * T::kSize, x);
+  }
+}
+
+template <class T, int DP> st_status forward_dim(st_seqs* s, AttnArgs a, hipStream_t st) {
+  constexpr int KT = T::kSize == 2 ? 64 : 32;
+  const AttnList& l = s->list[kListForward];
+  float* part = a.part;
+  for (int w = 0; w < 2; ++w) {
+    if (l.item[w].empty()) continue;
+    const int tile = l.tile[w];
+    a.items = l.d_item[w];
+    a.joins = l.d_join[w];
+    a.part = part;
+    a.part2 = part + l.parts[w] * s->kv_heads * tile * (int64_t)DP;
+    part = a.part2 + (l.parts[w] * s->kv_heads * tile + 63) / 64 * 64;
+    const int grid = (int)(l.item[w].size() * s->kv_heads);
+    if (w == 0) attn_forward<T, DP, KT, 4><<<grid, 256, 0, st>>>(a);
+    else attn_forward<T, DP, 32, 1><<<grid, 64, 0, st>>>(a);
+    st_status r = launch_check("attn_forward");
+    if (r != ST_OK) return r;
+    if (l.join[w].empty()) continue;
+    attn_join<T, DP><<<(int)(l.join[w].size() * s->kv_heads), 256, 0, st>>>(a, tile);
+    r = launch_check("attn_join");
+    if (r != ST_OK) return r;
+  }
+  return ST_OK;
+}
+
+}  // namespace
+
+size_t attn_forward_bytes(const st_seqs* s) {
+  size_t n = 0;
+  for (int w = 0; w < 2; ++w) {
+    const AttnList& l = s->list[kListForward];
+    const size_t rows = (size_t)(l.parts[w] * s->kv_heads * l.tile[w]);
+    n += rows * s->dp * sizeof(float) + (rows + 63) / 64 * 64 * sizeof(float);
+  }
+  return n;
+}
+
+// Checks and converts a tensor's view.  `span` tokens of one head's group must
+// lie within 31-bit byte offsets of each other (a tile's transfers).
+st_status attn_tensor(AttnTensor& out, const st_tokens* v, int64_t tokens, int heads, int dim, int esize, int span,
+                      const char* name) {
+  const std::string who(name);
+  if (!v) return fail(ST_ERR_INVALID_ARG, who + ": NULL argument");
+  if (tokens == 0) {
+    out = AttnTensor{nullptr, 0, 0};
+    return ST_OK;
+  }
+  if (!v->data) return fail(ST_ERR_INVALID_ARG, who + ": NULL data");
+  if (!aligned16(v->data)) return fail(ST_ERR_ALIGNMENT, who + ": data not 16-byte aligned");
+  // one token or one head has no stride: any value stands for it
+  const int64_t t = tokens == 1 ? (int64_t)dim * heads : v->token_stride;
+  const int64_t h = heads == 1 ? dim : v->head_stride;
+  if (t < 0 || h < 0) return fail(ST_ERR_INVALID_ARG, who + ": negative stride");
+  if (t > (1ll << 30) / ((int64_t)span * esize) || h > (1ll << 40))
+    return fail(ST_ERR_UNSUPPORTED, who + ": stride too large");
+  if ((t * esize) % 16 || (h * esize) % 16)
+    return fail(ST_ERR_ALIGNMENT, who + ": strides must be multiples of 16 bytes");
+  const bool by_token = tokens == 1 ? h >= dim : h >= dim && t >= (heads - 1) * h + dim;
+  const bool by_head = t >= dim && (heads == 1 || h >= (tokens - 1) * t + dim);
+  if (!by_token && !by_head) return fail(ST_ERR_BAD_SHAPE, who + ": rows overlap");
+  out = AttnTensor{static_cast<char*>(v->data), t * esize, h * esize};
+  return ST_OK;
+}
+
+}  // namespace st
+
+using namespace st;
+
+extern "C" {
+
+size_t st_attention_workspace_bytes(const st_seqs* seqs, int32_t backward) {
+  if (!seqs) return 0;
+  const size_t f = attn_forward_bytes(seqs);
+  return backward ? std::max(f, attn_backward_bytes(seqs)) : f;
+}
+
+st_status st_attention_packed(st_seqs* seqs, const st_tokens* q, const st_tokens* k, const st_tokens* v, float scale,
+                              const st_tokens* out, float* lse_or_null, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  auto err = [](st_status s, const std::string& m) { return fail(s, "st_attention_packed: " + m); };
+  if (!seqs || !q || !k || !v || !out) return err(ST_ERR_INVALID_ARG, "NULL argument");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return err(ST_ERR_INVALID_ARG, "scale must be positive and finite");
+  const int es = seqs->dtype == ST_F32 ? 4 : 2;
+  AttnArgs a{};
+  st_status s;
+  if ((s = attn_tensor(a.q, q, seqs->total_q, seqs->heads, seqs->dim, es, 1, "st_attention_packed: q")) != ST_OK ||
+      (s = attn_tensor(a.k, k, seqs->total_k, seqs->kv_heads, seqs->dim, es, 64, "st_attention_packed: k")) != ST_OK ||
+      (s = attn_tensor(a.v, v, seqs->total_k, seqs->kv_heads, seqs->dim, es, 64, "st_attention_packed: v")) != ST_OK ||
+      (s = attn_tensor(a.out, out, seqs->total_q, seqs->heads, seqs->dim, es, 1, "st_attention_packed: out")) != ST_OK)
+    return s;
+  if (!aligned16(lse_or_null) || !aligned16(workspace)) return err(ST_ERR_ALIGNMENT, "lse or workspace not 16-byte aligned");
+  const size_t need = attn_forward_bytes(seqs);
+  if (need && (!workspace || workspace_bytes < need)) return err(ST_ERR_WORKSPACE, "workspace missing or too small");
+  if (seqs->total_q == 0) return ok();
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  s = seqs_device_table(seqs, st);
+  if (s != ST_OK) return s;
+  a.lse = lse_or_null;
+  a.part = static_cast<float*>(workspace);
+  a.group = seqs->group;
+  a.by_group = div31((uint32_t)seqs->group);
+  a.kv_heads = seqs->kv_heads;
+  a.heads = seqs->heads;
+  a.dim = seqs->dim;
+  a.causal = seqs->causal;
+  a.scale = scale;
+  a.scale_log2 = scale * kLog2e;
+  if (seqs->dtype == ST_BF16) switch (seqs->dp) {
+      case 32: return forward_dim<BF16, 32>(seqs, a, st);
+      case 64: return forward_dim<BF16, 64>(seqs, a, st);
+      case 96: return forward_dim<BF16, 96>(seqs, a, st);
+      default: return forward_dim<BF16, 128>(seqs, a, st);
+    }
+  switch (seqs->dp) {
+    case 32: return forward_dim<F32, 32>(seqs, a, st);
+    case 64: return forward_dim<F32, 64>(seqs, a, st);
+    case 96: return forward_dim<F32, 96>(seqs, a, st);
+    default: return forward_dim<F32, 128>(seqs, a, st);
+  }
+}
+
+}  // extern "C"

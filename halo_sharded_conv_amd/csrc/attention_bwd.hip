@@ -1,0 +1,454 @@
+// Attention over packed sequences: backward.
+//
+// With p = exp(s - lse) of the forward pass, D = sum over channels of
+// dout * out, dp = dout v^T and ds = p * (dp - D):
+//   dv = p^T dout,   dk = scale * ds^T q,   dq = scale * ds k
+// Two kernels, each with its sums in registers from the first product to the
+// store: attn_dq walks the keys for a tile of rows, attn_dkv the rows for a
+// tile of keys.  The scores are formed in both (7 products where one kernel
+// would need 5), and in return no sum is ever added to memory by several
+// workgroups: no atomics, the same bits on every run.
+//
+// As in the forward pass a lane keeps one row (attn_dq) or one key (attn_dkv)
+// of every product, and p and ds go from product to product in registers.
+// Rows are (token, head of the group) pairs, so the gradients of a shared
+// key-value head are summed over its group inside attn_dkv's loop.
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "attention.h"
+
+namespace st {
+namespace {
+
+// ---------------------------------------------------------------------- dq
+
+template <class T, int DP, int KT, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void attn_dq(const AttnArgs a) {
+  using M = Mma<T>;
+  using Tl = Tile<T, DP, KT, NW>;
+  constexpr int KB = KT / 32, SR = Tl::SR, DB = Tl::DB, NI = Tl::NI;
+  __shared__ __attribute__((aligned(1024))) char k0s[Tl::BYTES];
+  __shared__ __attribute__((aligned(1024))) char v0s[Tl::BYTES];
+  __shared__ __attribute__((aligned(1024))) char k1s[Tl::BYTES];
+  __shared__ __attribute__((aligned(1024))) char v1s[Tl::BYTES];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, l32 = lane & 31;
+  const int kvh = blockIdx.x % a.kv_heads;
+  const AttnItem it = a.items[blockIdx.x / a.kv_heads];
+
+  const int row0 = it.at + wave * 32, row = row0 + l32;
+  const int token = (int)quo(row, a.by_group), head = kvh * a.group + row - token * a.group;
+  const bool live = token < it.lq;
+  const int off = it.lk - it.lq;
+  const int limit = a.causal ? min(it.lk, token + off + 1) : it.lk;
+  const int wave_limit = a.causal ? min(it.lk, (int)quo(row0, a.by_group) + off + 1) : it.lk;
+  const int wave_last = a.causal ? min(it.lk, (int)quo(row0 + 31, a.by_group) + off + 1) : it.lk;
+
+  typename M::Row qf[SR], gf[SR];
+  float delta = 0.f;
+  {
+    const char* pq = a.q.p + (int64_t)(it.q0 + token) * a.q.t + (int64_t)head * a.q.h;
+    const char* pg = a.dout.p + (int64_t)(it.q0 + token) * a.dout.t + (int64_t)head * a.dout.h;
+    const char* po = a.out.p + (int64_t)(it.q0 + token) * a.out.t + (int64_t)head * a.out.h;
+#pragma unroll
+    for (int s = 0; s < SR; ++s) {
+      const int byte = (2 * s + half) * 16;
+      const bool in = live && byte < a.dim * T::kSize;
+      qf[s] = in ? *reinterpret_cast<const typename M::Row*>(pq + byte) : typename M::Row{};
+      gf[s] = in ? *reinterpret_cast<const typename M::Row*>(pg + byte) : typename M::Row{};
+      const typename M::Row of = in ? *reinterpret_cast<const typename M::Row*>(po + byte) : typename M::Row{};
+#pragma unroll
+      for (int i = 0; i < 16 / T::kSize; ++i) delta = fmaf((float)gf[s][i], (float)of[i], delta);
+    }
+  }
+  delta = half_sum(delta);
+  const int64_t stat = (int64_t)(it.q0 + token) * a.heads + head;
+  // exp2(s - lse2): +inf (p = 0) for rows past the end and rows without keys
+  float lse2 = INFINITY;
+  if (live) {
+    lse2 = a.lse[stat] * kLog2e;
+    if (lse2 == -INFINITY) lse2 = INFINITY;
+    if (half == 0 && it.lo == 0) a.delta[stat] = delta;   // the tile's first part writes it
+  }
+  uint32_t koff[NI], voff[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int r = Tl::dma_row(wave, lane, i), b = Tl::dma_byte(wave, lane, i);
+    const bool in = b < a.dim * T::kSize;
+    koff[i] = in ? (uint32_t)(r * (int)a.k.t + b) : kOobOffset;
+    voff[i] = in ? (uint32_t)(r * (int)a.v.t + b) : kOobOffset;
+  }
+  const char* kb = a.k.p + (int64_t)it.k0 * a.k.t + (int64_t)kvh * a.k.h;
+  const char* vb = a.v.p + (int64_t)it.k0 * a.v.t + (int64_t)kvh * a.v.h;
+
+  f32x16 dq[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) dq[d] = f32x16{};
+
+  auto fetch = [&](char* ks, char* vs, int j0) __attribute__((always_inline)) {
+    const int64_t left = min(KT, it.hi - j0);
+    const auto rk = attn_rsrc(kb + (int64_t)j0 * a.k.t, left * a.k.t);
+    const auto rv = attn_rsrc(vb + (int64_t)j0 * a.v.t, left * a.v.t);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const uint32_t at = koff[i];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_void)Tl::dma_dst(ks, wave, i), 16, at, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const uint32_t at = voff[i];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_void)Tl::dma_dst(vs, wave, i), 16, at, 0, 0, 0);
+    }
+  };
+  auto step = [&](const char* ks, const char* vs, char* kn, char* vn, int j0) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+    if (j0 + KT < it.hi) fetch(kn, vn, j0 + KT);
+    if (j0 >= wave_last) return;
+    const bool masked = j0 + KT > wave_limit;
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+      f32x16 s = f32x16{}, dp = f32x16{};
+#pragma unroll
+      for (int c = 0; c < SR; ++c) {
+        s = M::rows(Tl::row(ks, b, c, lane), qf[c], s);
+        dp = M::rows(Tl::row(vs, b, c, lane), gf[c], dp);
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        dp[r] = exp2_hw(fmaf(s[r], a.scale_log2, -lse2)) * (dp[r] - delta);
+      if (masked) {
+        const int lim = limit - j0 - 4 * half;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (32 * b + 8 * (r / 4) + r % 4 >= lim) dp[r] = 0.f;
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const typename M::Col p = M::regs(dp, t);
+#pragma unroll
+        for (int d = 0; d < DB; ++d) dq[d] = M::cols(Tl::col(ks, b, t, d, lane), p, dq[d]);
+      }
+    }
+  };
+  if (it.lo < it.hi) {
+    fetch(k0s, v0s, it.lo);
+    for (int j = it.lo; j < it.hi; j += 2 * KT) {
+      step(k0s, v0s, k1s, v1s, j);
+      if (j + KT < it.hi) step(k1s, v1s, k0s, v0s, j + KT);
+    }
+  }
+  if (it.part >= 0) {
+    const int64_t slot = ((int64_t)it.part * a.kv_heads + kvh) * (32 * NW) + wave * 32 + l32;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+      store_block<F32>(reinterpret_cast<char*>(a.part + slot * DP), dq[d], a.scale, d, DP, lane);
+    return;
+  }
+  if (!live) return;
+  char* p = a.dq.p + (int64_t)(it.q0 + token) * a.dq.t + (int64_t)head * a.dq.h;
+#pragma unroll
+  for (int d = 0; d < DB; ++d) store_block<T>(p, dq[d], a.scale, d, a.dim, lane);
+}
+
+// ------------------------------------------------------------------ dk, dv
+
+template <class T, int DP, int RT, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void attn_dkv(const AttnArgs a) {
+  using M = Mma<T>;
+  using Tl = Tile<T, DP, RT, NW>;
+  constexpr int RB = RT / 32, SR = Tl::SR, DB = Tl::DB, NI = Tl::NI;
+  struct Stats { float lse2[RT], delta[RT]; int limit[RT]; };
+  __shared__ __attribute__((aligned(1024))) char q0s[Tl::BYTES];
+  __shared__ __attribute__((aligned(1024))) char g0s[Tl::BYTES];
+  __shared__ __attribute__((aligned(1024))) char q1s[Tl::BYTES];
+  __shared__ __attribute__((aligned(1024))) char g1s[Tl::BYTES];
+  __shared__ __attribute__((aligned(16))) Stats st0, st1;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = lane >> 5, l32 = lane & 31;
+  const int kvh = blockIdx.x % a.kv_heads;
+  const AttnItem it = a.items[blockIdx.x / a.kv_heads];
+  const int off = it.lk - it.lq;
+  const int key0 = it.at + wave * 32, key = key0 + l32;
+  const bool live = key < it.lk;
+
+  typename M::Row kf[SR], vf[SR];
+  {
+    const char* pk = a.k.p + (int64_t)(it.k0 + key) * a.k.t + (int64_t)kvh * a.k.h;
+    const char* pv = a.v.p + (int64_t)(it.k0 + key) * a.v.t + (int64_t)kvh * a.v.h;
+#pragma unroll
+    for (int s = 0; s < SR; ++s) {
+      const int byte = (2 * s + half) * 16;
+      const bool in = live && byte < a.dim * T::kSize;
+      kf[s] = in ? *reinterpret_cast<const typename M::Row*>(pk + byte) : typename M::Row{};
+      vf[s] = in ? *reinterpret_cast<const typename M::Row*>(pv + byte) : typename M::Row{};
+    }
+  }
+  f32x16 dk[DB], dv[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) { dk[d] = f32x16{}; dv[d] = f32x16{}; }
+
+  const char* qb = a.q.p + (int64_t)it.q0 * a.q.t + (int64_t)kvh * a.group * a.q.h;
+  const char* gb = a.dout.p + (int64_t)it.q0 * a.dout.t + (int64_t)kvh * a.group * a.dout.h;
+  const float* lb = a.lse + (int64_t)it.q0 * a.heads + kvh * a.group;
+  const float* db = a.delta + (int64_t)it.q0 * a.heads + kvh * a.group;
+
+  // rows [r0, r0 + RT): offsets from the tile's first token, zeros past the range
+  auto fetch = [&](char* qs, char* gs, int r0) __attribute__((always_inline)) {
+    const int t0 = __builtin_amdgcn_readfirstlane((int)quo(r0, a.by_group));
+    const auto rq = attn_rsrc(qb + (int64_t)t0 * a.q.t, 0x7FFFFFFF);
+    const auto rg = attn_rsrc(gb + (int64_t)t0 * a.dout.t, 0x7FFFFFFF);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = r0 + Tl::dma_row(wave, lane, i), b = Tl::dma_byte(wave, lane, i);
+      const int token = (int)quo(r, a.by_group), g = r - token * a.group;
+      const bool in = r < it.hi && b < a.dim * T::kSize;
+      const uint32_t oq = in ? (uint32_t)((token - t0) * (int)a.q.t + g * (int)a.q.h + b) : kOobOffset;
+      const uint32_t og = in ? (uint32_t)((token - t0) * (int)a.dout.t + g * (int)a.dout.h + b) : kOobOffset;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (lds_void)Tl::dma_dst(qs, wave, i), 16, oq, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rg, (lds_void)Tl::dma_dst(gs, wave, i), 16, og, 0, 0, 0);
+    }
+  };
+  // thread tid's row statistics of a tile: loaded ahead, put into LDS at the
+  // end of the step before
+  auto stats = [&](int r0, float& lse2, float& delta, int& limit) __attribute__((always_inline)) {
+    const int r = r0 + tid;
+    lse2 = INFINITY;                                    // p = 0: rows past the range, rows without keys
+    delta = 0.f;
+    limit = 0;
+    if (tid < RT && r < it.hi) {
+      const int token = (int)quo(r, a.by_group), g = r - token * a.group;
+      const int64_t at = (int64_t)token * a.heads + g;
+      lse2 = lb[at] * kLog2e;
+      if (lse2 == -INFINITY) lse2 = INFINITY;
+      delta = db[at];
+      limit = a.causal ? token + off + 1 : it.lk;
+    }
+  };
+  auto put = [&](Stats& s, float lse2, float delta, int limit) __attribute__((always_inline)) {
+    if (tid < RT) { s.lse2[tid] = lse2; s.delta[tid] = delta; s.limit[tid] = limit; }
+  };
+
+  auto step = [&](const char* qs, const char* gs, const Stats& sc, char* qn, char* gn, Stats& sn, int r0)
+      __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+    const bool more = r0 + RT < it.hi;
+    float lse2n, deltan;
+    int limitn;
+    if (more) {
+      fetch(qn, gn, r0 + RT);
+      stats(r0 + RT, lse2n, deltan, limitn);
+    }
+    // (uniform) rows below all of this wave's keys see none of them
+    const int last = min(it.hi, r0 + RT) - 1;
+    const bool some = !a.causal || key0 < (int)quo(last, a.by_group) + off + 1;
+    const bool masked = a.causal && key0 + 31 >= (int)quo(r0, a.by_group) + off + 1;
+    if (some) {
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        f32x16 s = f32x16{}, dp = f32x16{};
+#pragma unroll
+        for (int c = 0; c < SR; ++c) {
+          s = M::rows(Tl::row(qs, b, c, lane), kf[c], s);
+          dp = M::rows(Tl::row(gs, b, c, lane), vf[c], dp);
+        }
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const int at = 32 * b + 8 * r4 + 4 * half;
+          const f32x4_t l4 = *reinterpret_cast<const f32x4_t*>(&sc.lse2[at]);
+          const f32x4_t d4 = *reinterpret_cast<const f32x4_t*>(&sc.delta[at]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 4 * r4 + i;
+            s[r] = exp2_hw(fmaf(s[r], a.scale_log2, -l4[i]));
+            dp[r] = s[r] * (dp[r] - d4[i]);
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (key >= sc.limit[32 * b + 8 * (r / 4) + 4 * half + r % 4]) { s[r] = 0.f; dp[r] = 0.f; }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const typename M::Col p = M::regs(s, t), ds = M::regs(dp, t);
+#pragma unroll
+          for (int d = 0; d < DB; ++d) {
+            dv[d] = M::cols(Tl::col(gs, b, t, d, lane), p, dv[d]);
+            dk[d] = M::cols(Tl::col(qs, b, t, d, lane), ds, dk[d]);
+          }
+        }
+      }
+    }
+    if (more) put(sn, lse2n, deltan, limitn);
+  };
+
+  if (it.lo < it.hi) {
+    fetch(q0s, g0s, it.lo);
+    float lse2, delta;
+    int limit;
+    stats(it.lo, lse2, delta, limit);
+    put(st0, lse2, delta, limit);
+    for (int r = it.lo; r < it.hi; r += 2 * RT) {
+      step(q0s, g0s, st0, q1s, g1s, st1, r);
+      if (r + RT < it.hi) step(q1s, g1s, st1, q0s, g0s, st0, r + RT);
+    }
+  }
+  if (it.part >= 0) {
+    const int64_t slot = ((int64_t)it.part * a.kv_heads + kvh) * (32 * NW) + wave * 32 + l32;
+#pragma unroll
+    for (int d = 0; d < DB; ++d) {
+      store_block<F32>(reinterpret_cast<char*>(a.part + slot * DP), dk[d], a.scale, d, DP, lane);
+      store_block<F32>(reinterpret_cast<char*>(a.part2 + slot * DP), dv[d], 1.f, d, DP, lane);
+    }
+    return;
+  }
+  if (!live) return;
+  char* pk = a.dk.p + (int64_t)(it.k0 + key) * a.dk.t + (int64_t)kvh * a.dk.h;
+  char* pv = a.dv.p + (int64_t)(it.k0 + key) * a.dv.t + (int64_t)kvh * a.dv.h;
+#pragma unroll
+  for (int d = 0; d < DB; ++d) {
+    store_block<T>(pk, dk[d], a.scale, d, a.dim, lane);
+    store_block<T>(pv, dv[d], 1.f, d, a.dim, lane);
+  }
+}
+
+// Adds the parts of a split tile in order.  ROWS: dq (tile rows are query
+// rows); otherwise dk and dv (tile rows are keys).
+template <class T, int DP, bool ROWS>
+__global__ __launch_bounds__(256) void attn_add(const AttnArgs a, int tile) {
+  const int kvh = blockIdx.x % a.kv_heads;
+  const AttnJoin j = a.joins[blockIdx.x / a.kv_heads];
+  for (int i = threadIdx.x; i < tile * (DP / 4); i += 256) {
+    const int r = i / (DP / 4), c = i % (DP / 4) * 4, at = j.at + r;
+    const int token = ROWS ? (int)quo(at, a.by_group) : at;
+    if (token >= (ROWS ? j.lq : j.lk) || c >= a.dim) continue;
+    f32x4_t x = f32x4_t{}, y = f32x4_t{};
+#pragma unroll 4
+    for (int p = 0; p < j.count; ++p) {
+      const int64_t e = (((int64_t)(j.first + p) * a.kv_heads + kvh) * tile + r) * DP + c;
+      x += *reinterpret_cast<const f32x4_t*>(a.part + e);
+      if constexpr (!ROWS) y += *reinterpret_cast<const f32x4_t*>(a.part2 + e);
+    }
+    const float xv[4] = {x.x, x.y, x.z, x.w};
+    if constexpr (ROWS) {
+      const int head = kvh * a.group + at - token * a.group;
+      store_vec<T, 4>(a.dq.p + (int64_t)(j.q0 + token) * a.dq.t + (int64_t)head * a.dq.h + c * T::kSize, xv);
+    } else {
+      const float yv[4] = {y.x, y.y, y.z, y.w};
+      store_vec<T, 4>(a.dk.p + (int64_t)(j.k0 + at) * a.dk.t + (int64_t)kvh * a.dk.h + c * T::kSize, xv);
+      store_vec<T, 4>(a.dv.p + (int64_t)(j.k0 + at) * a.dv.t + (int64_t)kvh * a.dv.h + c * T::kSize, yv);
+    }
+  }
+}
+
+template <class T, int DP> st_status backward_dim(st_seqs* s, AttnArgs a, hipStream_t st) {
+  constexpr int KT = T::kSize == 2 ? 64 : 32;
+  for (int which : {kListDq, kListDkv}) {
+    const AttnList& l = s->list[which];
+    const bool rows = which == kListDq;
+    for (int w = 0; w < 2; ++w) {                       // one list at a time: they share the partial buffer
+      if (l.item[w].empty()) continue;
+      const int tile = l.tile[w];
+      a.items = l.d_item[w];
+      a.joins = l.d_join[w];
+      a.part2 = a.part + l.parts[w] * s->kv_heads * tile * (int64_t)DP;
+      const int grid = (int)(l.item[w].size() * s->kv_heads);
+      if (rows) {
+        if (w == 0) attn_dq<T, DP, KT, 4><<<grid, 256, 0, st>>>(a);
+        else attn_dq<T, DP, 32, 1><<<grid, 64, 0, st>>>(a);
+      } else {
+        if (w == 0) attn_dkv<T, DP, KT, 4><<<grid, 256, 0, st>>>(a);
+        else attn_dkv<T, DP, 32, 1><<<grid, 64, 0, st>>>(a);
+      }
+      st_status r = launch_check(rows ? "attn_dq" : "attn_dkv");
+      if (r != ST_OK) return r;
+      if (l.join[w].empty()) continue;
+      const int jg = (int)(l.join[w].size() * s->kv_heads);
+      if (rows) attn_add<T, DP, true><<<jg, 256, 0, st>>>(a, tile);
+      else attn_add<T, DP, false><<<jg, 256, 0, st>>>(a, tile);
+      r = launch_check("attn_add");
+      if (r != ST_OK) return r;
+    }
+  }
+  return ST_OK;
+}
+
+size_t delta_floats(const st_seqs* s) { return ((size_t)s->total_q * s->heads + 63) / 64 * 64; }
+
+}  // namespace
+
+size_t attn_backward_bytes(const st_seqs* s) {
+  size_t most = 0;
+  for (int w = 0; w < 2; ++w) {
+    const AttnList &q = s->list[kListDq], &k = s->list[kListDkv];
+    most = std::max(most, (size_t)(q.parts[w] * s->kv_heads * q.tile[w]) * s->dp);
+    most = std::max(most, (size_t)(k.parts[w] * s->kv_heads * k.tile[w]) * s->dp * 2);
+  }
+  return (delta_floats(s) + most) * sizeof(float);
+}
+
+}  // namespace st
+
+using namespace st;
+
+extern "C" st_status st_attention_packed_backward(st_seqs* seqs, const st_tokens* q, const st_tokens* k,
+                                                  const st_tokens* v, const st_tokens* out, const float* lse,
+                                                  const st_tokens* dout, float scale, const st_tokens* dq,
+                                                  const st_tokens* dk, const st_tokens* dv, void* workspace,
+                                                  size_t workspace_bytes, void* stream) {
+  auto err = [](st_status s, const std::string& m) { return fail(s, "st_attention_packed_backward: " + m); };
+  if (!seqs || !q || !k || !v || !out || !dout || !dq || !dk || !dv) return err(ST_ERR_INVALID_ARG, "NULL argument");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return err(ST_ERR_INVALID_ARG, "scale must be positive and finite");
+  const int es = seqs->dtype == ST_F32 ? 4 : 2, span = 64;
+  const int64_t tq = seqs->total_q, tk = seqs->total_k;
+  AttnArgs a{};
+  struct { AttnTensor* t; const st_tokens* v; bool keys; const char* name; } const all[] = {
+      {&a.q, q, false, "st_attention_packed_backward: q"},       {&a.k, k, true, "st_attention_packed_backward: k"},
+      {&a.v, v, true, "st_attention_packed_backward: v"},        {&a.out, out, false, "st_attention_packed_backward: out"},
+      {&a.dout, dout, false, "st_attention_packed_backward: dout"}, {&a.dq, dq, false, "st_attention_packed_backward: dq"},
+      {&a.dk, dk, true, "st_attention_packed_backward: dk"},     {&a.dv, dv, true, "st_attention_packed_backward: dv"}};
+  for (const auto& e : all) {
+    const st_status s = attn_tensor(*e.t, e.v, e.keys ? tk : tq, e.keys ? seqs->kv_heads : seqs->heads, seqs->dim, es, span, e.name);
+    if (s != ST_OK) return s;
+  }
+  // one group's heads lie within a tile's 31-bit offsets
+  for (const AttnTensor* t : {&a.q, &a.dout})
+    if (seqs->group > 1 && t->h >= (1ll << 30) / seqs->group)
+      return err(ST_ERR_UNSUPPORTED, "head stride of q or dout too large for grouped heads");
+  if (tq > 0 && !lse) return err(ST_ERR_INVALID_ARG, "NULL lse");
+  if (!aligned16(lse) || !aligned16(workspace)) return err(ST_ERR_ALIGNMENT, "lse or workspace not 16-byte aligned");
+  const size_t need = attn_backward_bytes(seqs);
+  if (need && (!workspace || workspace_bytes < need)) return err(ST_ERR_WORKSPACE, "workspace missing or too small");
+  if (tq == 0 && tk == 0) return ok();
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  st_status s = seqs_device_table(seqs, st);
+  if (s != ST_OK) return s;
+  a.lse = const_cast<float*>(lse);
+  a.delta = static_cast<float*>(workspace);
+  a.part = a.delta + delta_floats(seqs);
+  a.group = seqs->group;
+  a.by_group = div31((uint32_t)seqs->group);
+  a.kv_heads = seqs->kv_heads;
+  a.heads = seqs->heads;
+  a.dim = seqs->dim;
+  a.causal = seqs->causal;
+  a.scale = scale;
+  a.scale_log2 = scale * kLog2e;
+  if (seqs->dtype == ST_BF16) switch (seqs->dp) {
+      case 32: return backward_dim<BF16, 32>(seqs, a, st);
+      case 64: return backward_dim<BF16, 64>(seqs, a, st);
+      case 96: return backward_dim<BF16, 96>(seqs, a, st);
+      default: return backward_dim<BF16, 128>(seqs, a, st);
+    }
+  switch (seqs->dp) {
+    case 32: return backward_dim<F32, 32>(seqs, a, st);
+    case 64: return backward_dim<F32, 64>(seqs, a, st);
+    case 96: return backward_dim<F32, 96>(seqs, a, st);
+    default: return backward_dim<F32, 128>(seqs, a, st);
+  }
+}

@@ -576,6 +576,175 @@ st_status st_groupnorm_backward(const st_plan* y_plan, const float* const* y_buf
                                 float* dgamma_or_null, float* dbeta_or_null, void* workspace, size_t workspace_bytes,
                                 void* stream);
 
+/* -------------------------------------------------------------- layer norm */
+
+/*
+ * st_layernorm_sharded - layer norm over the C channels of every cell.
+ * Section 4 ("Results and benchmarks") of the ShardTensor summary runs
+ * transformers over the same sharded grids; their norm needs one cell only:
+ *   y = (x - mean) / sqrt(var + eps) * gamma_c + beta_c
+ * with the mean and the biased variance of that cell's channels, so there is
+ * no halo and no combine over shards.
+ *   x_plan, x_bufs      input shards, any halo (only interiors are read), fp32
+ *                       or bf16, C <= 16384
+ *   gamma/beta_or_null  C floats or NULL (1 and 0)
+ *   eps                 finite, >= 0
+ *   y_plan, y_bufs      output shards: same ndim, batch, channels and shard
+ *                       sizes as x_plan, any halo and dtype (only interiors are
+ *                       written); may be x_bufs themselves where both plans
+ *                       have one halo and dtype, otherwise must not overlap x
+ *   stats_or_null       2 floats (mean, 1 / sqrt(var + eps)) per cell, shard by
+ *                       shard, each shard's interior cells in memory order: what
+ *                       the backward pass reads
+ * Statistics are fp32 over registers (mean first, then the centred squares).  A
+ * cell's bits do not depend on the shard plan.
+ * Errors: ST_ERR_BAD_SHAPE (plans that differ), ST_ERR_UNSUPPORTED (C > 16384, a
+ * shard of 2^31 cells), ST_ERR_ALIGNMENT, ST_ERR_INVALID_ARG, ST_ERR_HIP.
+ */
+st_status st_layernorm_sharded(const st_plan* x_plan, const void* const* x_bufs, const float* gamma_or_null,
+                               const float* beta_or_null, float eps, const st_plan* y_plan, void* const* y_bufs,
+                               float* stats_or_null, void* stream);
+
+/*
+ * st_layernorm_backward - gradients of st_layernorm_sharded for dy:
+ *   dx     = r * (g - mean(g) - xhat * mean(g * xhat)),  g = dy * gamma_c
+ *   dgamma = sum over all cells of dy * xhat,  dbeta = sum of dy  (per channel)
+ *   x_plan, x_bufs      the forward call's input (read)
+ *   dy_plan, dy_bufs    upstream gradient, any halo and dtype (interiors read)
+ *   gamma_or_null       as in the forward call
+ *   stats               as the forward call wrote it
+ *   dx_plan, dx_bufs    gradient at x, any halo and dtype (interiors written),
+ *                       e.g. the padded bf16 shards an input-gradient conv
+ *                       reads; may be dy_bufs or x_bufs themselves where halo and
+ *                       dtype are theirs, otherwise must not overlap them
+ *   dgamma_or_null, dbeta_or_null   C floats each, or NULL (not computed)
+ *   workspace           >= st_layernorm_backward_workspace_bytes(x_plan) bytes
+ * dgamma and dbeta are summed in fp32 in an order fixed by the plan and the
+ * dtypes (no atomics).  All three plans share ndim, batch, channels and sizes.
+ */
+size_t st_layernorm_backward_workspace_bytes(const st_plan* x_plan);
+st_status st_layernorm_backward(const st_plan* x_plan, const void* const* x_bufs, const st_plan* dy_plan,
+                                const void* const* dy_bufs, const float* gamma_or_null, const float* stats,
+                                const st_plan* dx_plan, void* const* dx_bufs, float* dgamma_or_null,
+                                float* dbeta_or_null, void* workspace, size_t workspace_bytes, void* stream);
+
+/* -------------------------------------------------------- rotary positions */
+
+/*
+ * st_plan_positions - the global grid position of every cell of every shard:
+ * pos_bufs[s] receives int32 [N][extent...][ndim] (axis order of the plan), the
+ * shard's offset included, so tokens of different shards keep their places in
+ * the whole volume (section 2, "Design principles").
+ */
+st_status st_plan_positions(const st_plan* plan, int32_t* const* pos_bufs, void* stream);
+
+/*
+ * st_rope_axes - rotary positions with one section of channels per axis.
+ * Tokens are rows of `heads` heads of head_dim channels.  Axis a owns the
+ * next axis_dims[a] channels of a head (the rest, after all axes, is copied);
+ * pair i of its axis_dims[a] / 2 pairs turns by
+ * positions[token][a] * base^(-2 i / axis_dims[a]):
+ *   (u, v) -> (u cos - v sin, u sin + v cos)
+ *   x, x_dtype          input; head h of token t starts at element
+ *                       t * x_token_stride + h * x_head_stride
+ *   tokens              >= 0 (0: nothing is done), below 2^31
+ *   rotated_heads       heads below this one turn, the others are copied (a joint
+ *                       q, k, v projection turns q and k and copies v)
+ *   head_dim            even, at most 256
+ *   positions           int32 [tokens][naxes]
+ *   naxes, axis_dims    1 to 3 axes, even widths that add up to head_dim at most
+ *   base                > 1
+ *   pairs               ST_ROPE_HALVES: channels (i, i + d/2) of a section,
+ *                       ST_ROPE_ADJACENT: (2 i, 2 i + 1)
+ *   inverse             != 0: turn by the negative angle; this is the gradient
+ *   out, out_dtype      output in its own dtype and strides; may be x itself with
+ *                       the same dtype and strides, otherwise must not overlap x
+ * Angles are formed in 64 bits, the rotation in fp32.
+ * Errors: ST_ERR_UNSUPPORTED (axes, head_dim), ST_ERR_BAD_SHAPE (axis widths,
+ * output rows that overlap), ST_ERR_ALIGNMENT, ST_ERR_INVALID_ARG, ST_ERR_HIP.
+ */
+#define ST_ROPE_HALVES 0
+#define ST_ROPE_ADJACENT 1
+st_status st_rope_axes(const void* x, st_dtype x_dtype, int64_t x_token_stride, int64_t x_head_stride, int64_t tokens,
+                       int32_t heads, int32_t rotated_heads, int32_t head_dim, const int32_t* positions, int32_t naxes,
+                       const int32_t* axis_dims, double base, int32_t pairs, int32_t inverse, void* out,
+                       st_dtype out_dtype, int64_t out_token_stride, int64_t out_head_stride, void* stream);
+
+/* ----------------------------------------------------- packed attention */
+
+/*
+ * st_plan_sequences - the plan of attention over packed sequences (host only).
+ * Sequences lie back to back: queries of all sequences along one token axis,
+ * keys and values along another.
+ *   nseq                >= 1
+ *   q_lens, k_lens_or_null   tokens per sequence (>= 0; NULL: k_lens = q_lens)
+ *   heads, kv_heads     kv_heads divides heads; query head h reads key-value
+ *                       head h / (heads / kv_heads)
+ *   head_dim            a multiple of 8, at most ST_MAX_HEAD_DIM
+ *   dtype               element type of q, k, v, out and the gradients
+ *   causal              != 0: query i of lq sees keys 0 .. i + lk - lq (the last
+ *                       query sees the last key); rows may see no key at all
+ *   out                 receives the plan; release it with st_seqs_destroy
+ * The plan holds the work of every workgroup: tiles of rows or keys, long loops
+ * split over several workgroups where there are few tiles.  One plan serves any
+ * number of calls with the same lengths (all layers of a model, forward and
+ * backward).  st_seqs_upload is to it what st_plan_upload is to a shard plan.
+ */
+#define ST_MAX_HEAD_DIM 128
+typedef struct st_seqs st_seqs; /* opaque, library-owned */
+st_status st_plan_sequences(int32_t nseq, const int32_t* q_lens, const int32_t* k_lens_or_null, int32_t heads,
+                            int32_t kv_heads, int32_t head_dim, st_dtype dtype, int32_t causal, st_seqs** out);
+st_status st_seqs_destroy(st_seqs* seqs);
+st_status st_seqs_upload(st_seqs* seqs, void* stream);
+
+/* A packed tensor: head h of token t starts at element t * token_stride +
+ * h * head_stride; channels are contiguous.  data and both strides are
+ * multiples of 16 bytes. */
+typedef struct st_tokens {
+  void* data;
+  int64_t token_stride, head_stride;
+} st_tokens;
+
+/* Bytes of workspace of the forward call (backward == 0), or of either call. */
+size_t st_attention_workspace_bytes(const st_seqs* seqs, int32_t backward);
+
+/*
+ * st_attention_packed - out = softmax(scale * q k^T) v per sequence and head.
+ *   q, out              [total queries][heads][head_dim]
+ *   k, v                [total keys][kv_heads][head_dim]
+ *   scale               positive, finite
+ *   lse_or_null         [total queries][heads] floats: log of the softmax's
+ *                       denominator, sum of exp(scale * q k); the backward pass
+ *                       reads it
+ *   workspace           >= st_attention_workspace_bytes(seqs, 0) bytes
+ * A row that sees no key gives zeros and lse = -inf.  bf16 operands multiply on
+ * the matrix cores with fp32 accumulation (the weights rounded to bf16), fp32
+ * operands in fp32; scores, softmax statistics and sums are fp32.  Keys that a
+ * row does not see have no part in it, NaN and infinities included.  The
+ * result's bits depend on the plan only, not on timing.
+ * Errors: ST_ERR_WORKSPACE, ST_ERR_ALIGNMENT, ST_ERR_BAD_SHAPE (rows that
+ * overlap), ST_ERR_UNSUPPORTED (strides past 2^30 bytes a tile; first use inside
+ * a graph capture without st_seqs_upload), ST_ERR_INVALID_ARG, ST_ERR_HIP.
+ */
+st_status st_attention_packed(st_seqs* seqs, const st_tokens* q, const st_tokens* k, const st_tokens* v, float scale,
+                              const st_tokens* out, float* lse_or_null, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * st_attention_packed_backward - dq, dk, dv of st_attention_packed for dout.
+ *   q, k, v, out, lse   the forward call's inputs and outputs (read)
+ *   dout                gradient at out, laid out as out is described (read)
+ *   dq, dk, dv          gradients at q, k, v (written; must not overlap an input);
+ *                       dk and dv are summed over the query heads of their group
+ *   workspace           >= st_attention_workspace_bytes(seqs, 1) bytes
+ * No atomics: the bits depend on the plan only.  A NaN or infinity in a query,
+ * key or value reaches the gradients of its whole sequence, and no other one's.
+ */
+st_status st_attention_packed_backward(st_seqs* seqs, const st_tokens* q, const st_tokens* k, const st_tokens* v,
+                                       const st_tokens* out, const float* lse, const st_tokens* dout, float scale,
+                                       const st_tokens* dq, const st_tokens* dk, const st_tokens* dv, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
