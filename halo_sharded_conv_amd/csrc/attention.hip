@@ -17,6 +17,7 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 #include "attention.h"
 
@@ -27,54 +28,63 @@ namespace {
 // p stays below 2^8, and most tiles then scale nothing
 constexpr float kSlack = 8.f;
 
-// The parts of a V fragment that a matrix product must not see next to a zero
-// weight: 0 * inf and 0 * NaN are NaN, but a masked key has no weight at all.
+// What a matrix product must not see next to a zero weight: 0 * inf and 0 * NaN
+// are NaN, but a masked key has no weight at all.
 template <class T> struct Special;
 template <> struct Special<BF16> {
+  typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
   static __device__ __forceinline__ bool any(bf16x8 v) {
     const u32x4_t w = __builtin_bit_cast(u32x4_t, v);
     bool f = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f = f || (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
+    for (int i = 0; i < 4; ++i) f |= ((w[i] & 0x7F80u) == 0x7F80u) | ((w[i] & 0x7F800000u) == 0x7F800000u);
     return f;
   }
-  // kind 0: the finite values, 1: one where NaN, 2: one where +inf, 3: one where -inf
-  static __device__ __forceinline__ bf16x8 pick(bf16x8 v, int kind) {
-    typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-    const u16x8 w = __builtin_bit_cast(u16x8, v);
-    u16x8 o;
+  static __device__ __forceinline__ bf16x8 finite(bf16x8 v) {
+    u16x8 w = __builtin_bit_cast(u16x8, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint16_t b = w[i];
-      const bool inf = (b & 0x7FFF) == 0x7F80, nan = (b & 0x7FFF) > 0x7F80;
-      const bool one = kind == 1 ? nan : kind == 2 ? inf && !(b >> 15) : inf && (b >> 15);
-      o[i] = kind == 0 ? (inf || nan ? 0 : b) : (one ? 0x3F80 : 0);
-    }
-    return __builtin_bit_cast(bf16x8, o);
+    for (int i = 0; i < 8; ++i) w[i] = (w[i] & 0x7F80) == 0x7F80 ? 0 : w[i];
+    return __builtin_bit_cast(bf16x8, w);
   }
 };
 template <> struct Special<F32> {
   static __device__ __forceinline__ bool any(f32x8 v) {
     bool f = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f = f || (__float_as_uint(v[i]) & 0x7F800000u) == 0x7F800000u;
+    for (int i = 0; i < 8; ++i) f |= (__float_as_uint(v[i]) & 0x7F800000u) == 0x7F800000u;
     return f;
   }
-  static __device__ __forceinline__ f32x8 pick(f32x8 v, int kind) {
-    f32x8 o;
+  static __device__ __forceinline__ f32x8 finite(f32x8 v) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t b = __float_as_uint(v[i]);
-      const bool inf = (b & 0x7FFFFFFFu) == 0x7F800000u, nan = (b & 0x7FFFFFFFu) > 0x7F800000u;
-      const bool one = kind == 1 ? nan : kind == 2 ? inf && !(b >> 31) : inf && (b >> 31);
-      o[i] = kind == 0 ? (inf || nan ? 0.f : v[i]) : (one ? 1.f : 0.f);
-    }
-    return o;
+    for (int i = 0; i < 8; ++i) v[i] = (__float_as_uint(v[i]) & 0x7F800000u) == 0x7F800000u ? 0.f : v[i];
+    return v;
   }
 };
 
+// The NaN and infinities of four channels of V over the keys [j, end) that a
+// row sees (those below `limit`).  Every seen key has a weight above zero, so
+// they enter the row's sum as they are.
+template <class T>
+__device__ __attribute__((noinline)) f32x4_t special_keys(const char* v, int64_t stride, int j, int end, int limit, int c) {
+  f32x4_t x = f32x4_t{};
+  for (; j < end; ++j) {
+    float y[4];
+    load_vec<T, 4>(v + (int64_t)j * stride + c * T::kSize, y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] += j < limit && (__float_as_uint(y[i]) & 0x7F800000u) == 0x7F800000u ? y[i] : 0.f;
+  }
+  return x;
+}
+template <class T>
+__device__ __forceinline__ void special_sum(const char* v, int64_t stride, int j, int end, int limit, int c, int dim, float (&x)[4]) {
+  f32x4_t y = f32x4_t{};
+  if (c < dim) y = special_keys<T>(v, stride, j, end, limit, c);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = y[i];
+}
+
 template <class T, int DP, int KT, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void attn_forward(const AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, DP * T::kSize > 256 ? 1 : 2) void attn_forward(const AttnArgs a) {
   using M = Mma<T>;
   using Tl = Tile<T, DP, KT, NW>;
   constexpr int KB = KT / 32, SR = Tl::SR, DB = Tl::DB, NI = Tl::NI;
@@ -94,8 +104,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_forward(const AttnArgs a) {
   const int off = it.lk - it.lq;                        // causal: token i sees keys <= i + off
   // keys below `limit` are seen by this lane's row
   const int limit = a.causal ? min(it.lk, token + off + 1) : it.lk;
-  const int wave_token = (int)quo(row0, a.by_group);    // lowest limit of the wave
-  const int wave_limit = a.causal ? min(it.lk, wave_token + off + 1) : it.lk;
+  // every row of the workgroup sees the keys below `all`; no row of this wave
+  // sees one at or past `wave_last`
+  const int all = min(it.hi, a.causal ? (int)quo(it.at, a.by_group) + off + 1 : it.lk);
   const int wave_last = a.causal ? min(it.lk, (int)quo(row0 + 31, a.by_group) + off + 1) : it.lk;
 
   typename M::Row qf[SR];
@@ -123,6 +134,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_forward(const AttnArgs a) {
 #pragma unroll
   for (int d = 0; d < DB; ++d) o[d] = f32x16{};
   float m = -INFINITY, l = 0.f;
+  bool sp = false;                                      // this lane met a NaN or an infinity there
 
   auto fetch = [&](char* ks, char* vs, int j0) __attribute__((always_inline)) {
     const int64_t left = min(KT, it.hi - j0);            // rows past the range read zeros
@@ -140,11 +152,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_forward(const AttnArgs a) {
     }
   };
 
-  auto step = [&](const char* ks, const char* vs, char* kn, char* vn, int j0) __attribute__((always_inline)) {
+  // one tile: MASKED where some row may not see some key of it
+  auto step = [&](auto MASKED, const char* ks, const char* vs, char* kn, char* vn, int j0) __attribute__((always_inline)) {
+    constexpr bool masked = decltype(MASKED)::value;
     __builtin_amdgcn_s_waitcnt(0x0F70);                 // vmcnt(0): this tile is in LDS
     __syncthreads();                                    // ... for every wave; the other tile is free
     if (j0 + KT < it.hi) fetch(kn, vn, j0 + KT);
-    if (j0 >= wave_last) return;                        // (uniform) nothing here is seen by these rows
+    if (masked && j0 >= wave_last) return;              // (uniform) nothing here is seen by these rows
     f32x16 s[KB];
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
@@ -152,8 +166,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_forward(const AttnArgs a) {
 #pragma unroll
       for (int c = 0; c < SR; ++c) s[b] = M::rows(Tl::row(ks, b, c, lane), qf[c], s[b]);
     }
-    const bool masked = j0 + KT > wave_limit;
-    if (masked) {
+    if constexpr (masked) {
       const int lim = limit - j0 - 4 * half;
 #pragma unroll
       for (int b = 0; b < KB; ++b)
@@ -173,9 +186,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_forward(const AttnArgs a) {
       m = mn;
       l *= f;
 #pragma unroll
-      for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[d][r] *= f;
+      for (int d = 0; d < DB; ++d) o[d] *= f;
     }
     const float ms = m == -INFINITY ? 0.f : m;          // no key seen so far: p = 0
 #pragma unroll
@@ -185,89 +196,73 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_forward(const AttnArgs a) {
         s[b][r] = exp2_hw(fmaf(s[b][r], a.scale_log2, -ms));
         l += s[b][r];
       }
-    if (masked && a.causal) {
-      // a later key's NaN or infinity has no part in an earlier row
-      bool sp = false;
-#pragma unroll
-      for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) sp |= Special<T>::any(Tl::col(vs, b, t, d, lane));
-      if (__any(sp)) {
-        const int lim = limit - j0 - 4 * half;
-        for (int d = 0; d < DB; ++d) {
-          f32x16 cn = f32x16{}, cp = f32x16{}, cm = f32x16{}, od = o[0];
-#pragma unroll
-          for (int e = 1; e < DB; ++e) od = d == e ? o[e] : od;
-#pragma unroll
-          for (int b = 0; b < KB; ++b)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              f32x16 seen, pos, zero;
-#pragma unroll
-              for (int r = 0; r < 16; ++r) {
-                const bool vis = 32 * b + 8 * (r / 4) + r % 4 < lim;
-                seen[r] = vis ? 1.f : 0.f;
-                pos[r] = vis && s[b][r] > 0.f ? 1.f : 0.f;
-                zero[r] = vis && !(s[b][r] > 0.f) ? 1.f : 0.f;
-              }
-              const typename M::Col w = Tl::col(vs, b, t, d, lane);
-              const typename M::Col pinf = Special<T>::pick(w, 2), minf = Special<T>::pick(w, 3);
-              od = M::cols(Special<T>::pick(w, 0), M::regs(s[b], t), od);
-              cn = M::cols(Special<T>::pick(w, 1), M::regs(seen, t), cn);
-              cn = M::cols(pinf, M::regs(zero, t), cn);
-              cn = M::cols(minf, M::regs(zero, t), cn);
-              cp = M::cols(pinf, M::regs(pos, t), cp);
-              cm = M::cols(minf, M::regs(pos, t), cm);
-            }
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            if (cp[r] > 0.f) od[r] += INFINITY;
-            if (cm[r] > 0.f) od[r] -= INFINITY;
-            if (cn[r] > 0.f) od[r] = NAN;
-          }
-#pragma unroll
-          for (int e = 0; e < DB; ++e)
-            if (d == e) o[e] = od;
-        }
-        return;
-      }
-    }
+    // a hidden key's NaN or infinity has no part in a row: a masked tile's product
+    // takes the finite values, what is left is added to the rows that see it at
+    // the end (special_sum)
 #pragma unroll
     for (int b = 0; b < KB; ++b)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const typename M::Col p = M::regs(s[b], t);
 #pragma unroll
-        for (int d = 0; d < DB; ++d) o[d] = M::cols(Tl::col(vs, b, t, d, lane), p, o[d]);
+        for (int d = 0; d < DB; ++d) {
+          typename M::Col w = Tl::col(vs, b, t, d, lane);
+          if constexpr (masked) {
+            sp |= Special<T>::any(w);
+            w = Special<T>::finite(w);
+          }
+          o[d] = M::cols(w, p, o[d]);
+        }
+        if constexpr (masked) __builtin_amdgcn_sched_barrier(0);
       }
   };
 
+  // whole tiles that every row sees, in pairs, then the rest with the mask
+  const int first_masked = it.lo + max(0, (all - it.lo) / (2 * KT)) * (2 * KT);
   if (it.lo < it.hi) {
     fetch(k0s, v0s, it.lo);
-    for (int j = it.lo; j < it.hi; j += 2 * KT) {
-      step(k0s, v0s, k1s, v1s, j);
-      if (j + KT < it.hi) step(k1s, v1s, k0s, v0s, j + KT);
+    int j = it.lo;
+    for (; j < first_masked; j += 2 * KT) {
+      step(std::false_type{}, k0s, v0s, k1s, v1s, j);
+      step(std::false_type{}, k1s, v1s, k0s, v0s, j + KT);
+    }
+    for (; j < it.hi; j += 2 * KT) {
+      step(std::true_type{}, k0s, v0s, k1s, v1s, j);
+      if (j + KT < it.hi) step(std::true_type{}, k1s, v1s, k0s, v0s, j + KT);
     }
   }
 
   l = half_sum(l);
   const float inv = l == 0.f ? 0.f : 1.f / l;           // a row that sees no key: zeros
-  if (it.part >= 0) {
-    const int64_t slot = ((int64_t)it.part * a.kv_heads + kvh) * (32 * NW) + wave * 32 + l32;
-    if (half == 0) a.part2[slot] = l == 0.f ? -INFINITY : m + log2f(l);
+  const bool split = it.part >= 0;
+  const int64_t slot = split ? ((int64_t)it.part * a.kv_heads + kvh) * (32 * NW) + wave * 32 + l32 : 0;
+  const int64_t stat = (int64_t)(it.q0 + token) * a.heads + head;
+  if (half == 0) {
+    const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+    if (split) a.part2[slot] = lse2;
+    else if (live && a.lse) a.lse[stat] = lse2 * kLn2;
+  }
+  char* po = split ? reinterpret_cast<char*>(a.part + slot * DP)
+                   : a.out.p + (int64_t)(it.q0 + token) * a.out.t + (int64_t)head * a.out.h;
+  if (__any(sp)) {
 #pragma unroll
     for (int d = 0; d < DB; ++d)
-      store_block<F32>(reinterpret_cast<char*>(a.part + slot * DP), o[d], inv, d, DP, lane);
-    return;
-  }
-  if (!live) return;
-  if (half == 0 && a.lse)
-    a.lse[(int64_t)(it.q0 + token) * a.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-  char* po = a.out.p + (int64_t)(it.q0 + token) * a.out.t + (int64_t)head * a.out.h;
 #pragma unroll
-  for (int d = 0; d < DB; ++d) store_block<T>(po, o[d], inv, d, a.dim, lane);
+      for (int r4 = 0; r4 < 4; ++r4) {
+        const int c = reg_channel(d, r4, lane);
+        float x[4];
+        special_sum<T>(vb, a.v.t, first_masked, min(it.hi, wave_last), limit, c, a.dim, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[d][4 * r4 + i] += x[i];
+      }
+  }
+  if (split) {
+#pragma unroll
+    for (int d = 0; d < DB; ++d) store_block<F32>(po, o[d], inv, d, DP, lane);
+  } else if (live) {
+#pragma unroll
+    for (int d = 0; d < DB; ++d) store_block<T>(po, o[d], inv, d, a.dim, lane);
+  }
 }
 
 // Joins the parts of a tile whose keys were split: each part is a softmax of its
@@ -292,7 +287,10 @@ __global__ __launch_bounds__(256) void attn_join(const AttnArgs a, int tile) {
       const int64_t slot = ((int64_t)(j.first + p) * a.kv_heads + kvh) * tile + r;
       const float w = exp2_hw(a.part2[slot] - ms);
       l += w;
-      o += w * *reinterpret_cast<const f32x4_t*>(a.part + slot * DP + c);
+      const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part + slot * DP + c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)                       // a weight is above zero, underflow or not
+        o[e] += (__float_as_uint(x[e]) & 0x7F800000u) == 0x7F800000u ? x[e] : w * x[e];
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t tok = j.q0 + token;

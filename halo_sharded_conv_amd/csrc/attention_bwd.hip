@@ -25,7 +25,7 @@ namespace {
 // ---------------------------------------------------------------------- dq
 
 template <class T, int DP, int KT, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void attn_dq(const AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, DP * T::kSize > 256 ? 1 : 2) void attn_dq(const AttnArgs a) {
   using M = Mma<T>;
   using Tl = Tile<T, DP, KT, NW>;
   constexpr int KB = KT / 32, SR = Tl::SR, DB = Tl::DB, NI = Tl::NI;
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dq(const AttnArgs a) {
 // ------------------------------------------------------------------ dk, dv
 
 template <class T, int DP, int RT, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void attn_dkv(const AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, DP * T::kSize > 128 ? 1 : 2) void attn_dkv(const AttnArgs a) {
   using M = Mma<T>;
   using Tl = Tile<T, DP, RT, NW>;
   constexpr int RB = RT / 32, SR = Tl::SR, DB = Tl::DB, NI = Tl::NI;
