@@ -267,37 +267,57 @@ __global__ __launch_bounds__(64 * NW, DP * T::kSize > 256 ? 1 : 2) void attn_for
 
 // Joins the parts of a tile whose keys were split: each part is a softmax of its
 // own with log2 of its denominator, so the whole is their sum weighted by
-// 2^(part - max).  A thread takes four channels of one row.
+// 2^(part - max).  A workgroup takes one row: DP / 4 threads hold four channels
+// each, 1024 / DP of them add every so-many-th part, then their sums in order.
 template <class T, int DP>
 __global__ __launch_bounds__(256) void attn_join(const AttnArgs a, int tile) {
-  const int kvh = blockIdx.x % a.kv_heads;
-  const AttnJoin j = a.joins[blockIdx.x / a.kv_heads];
-  for (int i = threadIdx.x; i < tile * (DP / 4); i += 256) {
-    const int r = i / (DP / 4), c = i % (DP / 4) * 4;
-    const int row = j.at + r, token = (int)quo(row, a.by_group), head = kvh * a.group + row - token * a.group;
-    if (token >= j.lq || c >= a.dim) continue;
-    float m = -INFINITY;
-    for (int p = 0; p < j.count; ++p)
-      m = fmaxf(m, a.part2[((int64_t)(j.first + p) * a.kv_heads + kvh) * tile + r]);
-    const float ms = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    f32x4_t o = f32x4_t{};
+  constexpr int CT = DP / 4, LANES = 256 / CT;
+  __shared__ f32x4_t acc[LANES][CT];
+  __shared__ float red[4], den[LANES];
+  const int r = blockIdx.x % tile, unit = blockIdx.x / tile;
+  const int kvh = unit % a.kv_heads;
+  const AttnJoin j = a.joins[unit / a.kv_heads];
+  const int row = j.at + r, token = (int)quo(row, a.by_group), head = kvh * a.group + row - token * a.group;
+  if (token >= j.lq) return;
+  const int64_t first = ((int64_t)j.first * a.kv_heads + kvh) * tile + r, pitch = (int64_t)a.kv_heads * tile;
+  float m = -INFINITY;
+  for (int p = threadIdx.x; p < j.count; p += 256) m = fmaxf(m, a.part2[first + p * pitch]);
+  for (int i = 1; i < 64; i <<= 1) m = fmaxf(m, __shfl_xor(m, i));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float ms = m == -INFINITY ? 0.f : m;
+  const int ct = threadIdx.x % CT, g = threadIdx.x / CT;
+  float l = 0.f;
+  f32x4_t o = f32x4_t{};
+  if (g < LANES) {
 #pragma unroll 4
-    for (int p = 0; p < j.count; ++p) {
-      const int64_t slot = ((int64_t)(j.first + p) * a.kv_heads + kvh) * tile + r;
+    for (int p = g; p < j.count; p += LANES) {
+      const int64_t slot = first + p * pitch;
       const float w = exp2_hw(a.part2[slot] - ms);
+      const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part + slot * DP + 4 * ct);
       l += w;
-      const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part + slot * DP + c);
 #pragma unroll
       for (int e = 0; e < 4; ++e)                       // a weight is above zero, underflow or not
         o[e] += (__float_as_uint(x[e]) & 0x7F800000u) == 0x7F800000u ? x[e] : w * x[e];
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t tok = j.q0 + token;
-    if (c == 0 && a.lse) a.lse[tok * a.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    const float x[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-    store_vec<T, 4>(a.out.p + tok * a.out.t + (int64_t)head * a.out.h + c * T::kSize, x);
+    acc[g][ct] = o;
+    if (ct == 0) den[g] = l;
   }
+  __syncthreads();
+  if (threadIdx.x >= CT) return;
+  l = 0.f;
+  o = f32x4_t{};
+  const int n = min(LANES, j.count);
+  for (int i = 0; i < n; ++i) {
+    l += den[i];
+    o += acc[i][ct];
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t tok = j.q0 + token;
+  if (threadIdx.x == 0 && a.lse) a.lse[tok * a.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  const float x[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+  if (4 * ct < a.dim) store_vec<T, 4>(a.out.p + tok * a.out.t + (int64_t)head * a.out.h + 4 * ct * T::kSize, x);
 }
 
 template <class T, int DP> st_status forward_dim(st_seqs* s, AttnArgs a, hipStream_t st) {
@@ -318,7 +338,7 @@ template <class T, int DP> st_status forward_dim(st_seqs* s, AttnArgs a, hipStre
     st_status r = launch_check("attn_forward");
     if (r != ST_OK) return r;
     if (l.join[w].empty()) continue;
-    attn_join<T, DP><<<(int)(l.join[w].size() * s->kv_heads), 256, 0, st>>>(a, tile);
+    attn_join<T, DP><<<(int)(l.join[w].size() * s->kv_heads * tile), 256, 0, st>>>(a, tile);
     r = launch_check("attn_join");
     if (r != ST_OK) return r;
   }

@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 #include "attention.h"
 
@@ -43,7 +44,7 @@ __global__ __launch_bounds__(64 * NW, DP * T::kSize > 256 ? 1 : 2) void attn_dq(
   const bool live = token < it.lq;
   const int off = it.lk - it.lq;
   const int limit = a.causal ? min(it.lk, token + off + 1) : it.lk;
-  const int wave_limit = a.causal ? min(it.lk, (int)quo(row0, a.by_group) + off + 1) : it.lk;
+  const int all = min(it.hi, a.causal ? (int)quo(it.at, a.by_group) + off + 1 : it.lk);   // seen by every row
   const int wave_last = a.causal ? min(it.lk, (int)quo(row0 + 31, a.by_group) + off + 1) : it.lk;
 
   typename M::Row qf[SR], gf[SR];
@@ -102,12 +103,12 @@ __global__ __launch_bounds__(64 * NW, DP * T::kSize > 256 ? 1 : 2) void attn_dq(
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_void)Tl::dma_dst(vs, wave, i), 16, at, 0, 0, 0);
     }
   };
-  auto step = [&](const char* ks, const char* vs, char* kn, char* vn, int j0) __attribute__((always_inline)) {
+  auto step = [&](auto MASKED, const char* ks, const char* vs, char* kn, char* vn, int j0) __attribute__((always_inline)) {
+    constexpr bool masked = decltype(MASKED)::value;
     __builtin_amdgcn_s_waitcnt(0x0F70);
     __syncthreads();
     if (j0 + KT < it.hi) fetch(kn, vn, j0 + KT);
-    if (j0 >= wave_last) return;
-    const bool masked = j0 + KT > wave_limit;
+    if (masked && j0 >= wave_last) return;
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
       f32x16 s = f32x16{}, dp = f32x16{};
@@ -119,7 +120,7 @@ __global__ __launch_bounds__(64 * NW, DP * T::kSize > 256 ? 1 : 2) void attn_dq(
 #pragma unroll
       for (int r = 0; r < 16; ++r)
         dp[r] = exp2_hw(fmaf(s[r], a.scale_log2, -lse2)) * (dp[r] - delta);
-      if (masked) {
+      if constexpr (masked) {
         const int lim = limit - j0 - 4 * half;
 #pragma unroll
         for (int r = 0; r < 16; ++r)
@@ -135,9 +136,15 @@ __global__ __launch_bounds__(64 * NW, DP * T::kSize > 256 ? 1 : 2) void attn_dq(
   };
   if (it.lo < it.hi) {
     fetch(k0s, v0s, it.lo);
-    for (int j = it.lo; j < it.hi; j += 2 * KT) {
-      step(k0s, v0s, k1s, v1s, j);
-      if (j + KT < it.hi) step(k1s, v1s, k0s, v0s, j + KT);
+    const int first_masked = it.lo + max(0, (all - it.lo) / (2 * KT)) * (2 * KT);
+    int j = it.lo;
+    for (; j < first_masked; j += 2 * KT) {
+      step(std::false_type{}, k0s, v0s, k1s, v1s, j);
+      step(std::false_type{}, k1s, v1s, k0s, v0s, j + KT);
+    }
+    for (; j < it.hi; j += 2 * KT) {
+      step(std::true_type{}, k0s, v0s, k1s, v1s, j);
+      if (j + KT < it.hi) step(std::true_type{}, k1s, v1s, k0s, v0s, j + KT);
     }
   }
   if (it.part >= 0) {
@@ -155,11 +162,16 @@ __global__ __launch_bounds__(64 * NW, DP * T::kSize > 256 ? 1 : 2) void attn_dq(
 
 // ------------------------------------------------------------------ dk, dv
 
+// waves per SIMD that the registers allow: K, V and the sums of dk and dv
+template <class T, int DP> constexpr int dkv_waves() { return DP * T::kSize > 128 ? 1 : 2; }
+
 template <class T, int DP, int RT, int NW>
-__global__ __launch_bounds__(64 * NW, DP * T::kSize > 128 ? 1 : 2) void attn_dkv(const AttnArgs a) {
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(dkv_waves<T, DP>(), dkv_waves<T, DP>())))
+void attn_dkv(const AttnArgs a) {
   using M = Mma<T>;
   using Tl = Tile<T, DP, RT, NW>;
   constexpr int RB = RT / 32, SR = Tl::SR, DB = Tl::DB, NI = Tl::NI;
+  constexpr bool PIPE = T::kSize == 2 && RB == 2 && dkv_waves<T, DP>() == 1;
   struct Stats { float lse2[RT], delta[RT]; int limit[RT]; };
   __shared__ __attribute__((aligned(1024))) char q0s[Tl::BYTES];
   __shared__ __attribute__((aligned(1024))) char g0s[Tl::BYTES];
@@ -196,6 +208,12 @@ __global__ __launch_bounds__(64 * NW, DP * T::kSize > 128 ? 1 : 2) void attn_dkv
   const float* lb = a.lse + (int64_t)it.q0 * a.heads + kvh * a.group;
   const float* db = a.delta + (int64_t)it.q0 * a.heads + kvh * a.group;
 
+  uint32_t byte[NI];                                    // this lane's byte of a row per transfer
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int b = Tl::dma_byte(wave, lane, i);
+    byte[i] = b < a.dim * T::kSize ? (uint32_t)b : kOobOffset;
+  }
   // rows [r0, r0 + RT): offsets from the tile's first token, zeros past the range
   auto fetch = [&](char* qs, char* gs, int r0) __attribute__((always_inline)) {
     const int t0 = __builtin_amdgcn_readfirstlane((int)quo(r0, a.by_group));
@@ -203,59 +221,62 @@ __global__ __launch_bounds__(64 * NW, DP * T::kSize > 128 ? 1 : 2) void attn_dkv
     const auto rg = attn_rsrc(gb + (int64_t)t0 * a.dout.t, 0x7FFFFFFF);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int r = r0 + Tl::dma_row(wave, lane, i), b = Tl::dma_byte(wave, lane, i);
+      const int r = r0 + Tl::dma_row(wave, lane, i);
       const int token = (int)quo(r, a.by_group), g = r - token * a.group;
-      const bool in = r < it.hi && b < a.dim * T::kSize;
-      const uint32_t oq = in ? (uint32_t)((token - t0) * (int)a.q.t + g * (int)a.q.h + b) : kOobOffset;
-      const uint32_t og = in ? (uint32_t)((token - t0) * (int)a.dout.t + g * (int)a.dout.h + b) : kOobOffset;
+      const uint32_t tq = (uint32_t)((token - t0) * (int)a.q.t + g * (int)a.q.h) + byte[i];
+      const uint32_t tg = (uint32_t)((token - t0) * (int)a.dout.t + g * (int)a.dout.h) + byte[i];
+      const uint32_t oq = r < it.hi ? tq : kOobOffset, og = r < it.hi ? tg : kOobOffset;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (lds_void)Tl::dma_dst(qs, wave, i), 16, oq, 0, 0, 0);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rg, (lds_void)Tl::dma_dst(gs, wave, i), 16, og, 0, 0, 0);
     }
   };
   // thread tid's row statistics of a tile: loaded ahead, put into LDS at the
   // end of the step before
-  auto stats = [&](int r0, float& lse2, float& delta, int& limit) __attribute__((always_inline)) {
+  auto stats = [&](int r0, float& lse, float& delta) __attribute__((always_inline)) {
     const int r = r0 + tid;
-    lse2 = INFINITY;                                    // p = 0: rows past the range, rows without keys
+    lse = -INFINITY;
     delta = 0.f;
-    limit = 0;
     if (tid < RT && r < it.hi) {
       const int token = (int)quo(r, a.by_group), g = r - token * a.group;
       const int64_t at = (int64_t)token * a.heads + g;
-      lse2 = lb[at] * kLog2e;
-      if (lse2 == -INFINITY) lse2 = INFINITY;
+      lse = lb[at];
       delta = db[at];
-      limit = a.causal ? token + off + 1 : it.lk;
     }
   };
-  auto put = [&](Stats& s, float lse2, float delta, int limit) __attribute__((always_inline)) {
-    if (tid < RT) { s.lse2[tid] = lse2; s.delta[tid] = delta; s.limit[tid] = limit; }
+  auto put = [&](Stats& s, int r0, float lse, float delta) __attribute__((always_inline)) {
+    if (tid < RT) {
+      // p = 0 for rows past the range and rows without keys
+      s.lse2[tid] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+      s.delta[tid] = delta;
+      s.limit[tid] = a.causal ? (int)quo(r0 + tid, a.by_group) + off + 1 : it.lk;
+    }
   };
 
-  auto step = [&](const char* qs, const char* gs, const Stats& sc, char* qn, char* gn, Stats& sn, int r0)
+  // one tile: MASKED where some row may not see some key
+  auto step = [&](auto MASKED, const char* qs, const char* gs, const Stats& sc, char* qn, char* gn, Stats& sn, int r0)
       __attribute__((always_inline)) {
+    constexpr bool masked = decltype(MASKED)::value;
     __builtin_amdgcn_s_waitcnt(0x0F70);
     __syncthreads();
     const bool more = r0 + RT < it.hi;
-    float lse2n, deltan;
-    int limitn;
+    float lsen, deltan;
     if (more) {
       fetch(qn, gn, r0 + RT);
-      stats(r0 + RT, lse2n, deltan, limitn);
+      stats(r0 + RT, lsen, deltan);
     }
     // (uniform) rows below all of this wave's keys see none of them
     const int last = min(it.hi, r0 + RT) - 1;
-    const bool some = !a.causal || key0 < (int)quo(last, a.by_group) + off + 1;
-    const bool masked = a.causal && key0 + 31 >= (int)quo(r0, a.by_group) + off + 1;
-    if (some) {
-#pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        f32x16 s = f32x16{}, dp = f32x16{};
+    {
+      auto scores = [&](int b, f32x16& s, f32x16& dp) __attribute__((always_inline)) {
+        s = f32x16{};
+        dp = f32x16{};
 #pragma unroll
         for (int c = 0; c < SR; ++c) {
           s = M::rows(Tl::row(qs, b, c, lane), kf[c], s);
           dp = M::rows(Tl::row(gs, b, c, lane), vf[c], dp);
         }
+      };
+      auto weights = [&](int b, f32x16& s, f32x16& dp) __attribute__((always_inline)) {   // s -> p, dp -> ds
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
           const int at = 32 * b + 8 * r4 + 4 * half;
@@ -266,13 +287,12 @@ __global__ __launch_bounds__(64 * NW, DP * T::kSize > 128 ? 1 : 2) void attn_dkv
             const int r = 4 * r4 + i;
             s[r] = exp2_hw(fmaf(s[r], a.scale_log2, -l4[i]));
             dp[r] = s[r] * (dp[r] - d4[i]);
+            if constexpr (masked)
+              if (key >= sc.limit[at + i]) { s[r] = 0.f; dp[r] = 0.f; }
           }
         }
-        if (masked) {
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (key >= sc.limit[32 * b + 8 * (r / 4) + 4 * half + r % 4]) { s[r] = 0.f; dp[r] = 0.f; }
-        }
+      };
+      auto sums = [&](int b, const f32x16& s, const f32x16& dp) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const typename M::Col p = M::regs(s, t), ds = M::regs(dp, t);
@@ -282,21 +302,99 @@ __global__ __launch_bounds__(64 * NW, DP * T::kSize > 128 ? 1 : 2) void attn_dkv
             dk[d] = M::cols(Tl::col(qs, b, t, d, lane), ds, dk[d]);
           }
         }
+      };
+      if constexpr (PIPE && !masked) {
+        // One wave per SIMD hides nothing by itself: the order is written out.
+        // A chunk is two products, the LDS reads of the chunk after the next,
+        // and, under the products of the other block, two exponentials; a
+        // barrier to the compiler's scheduler keeps each chunk together.
+        constexpr int C2 = 2 * DB;                      // chunks of a block's sums
+        f32x16 s0 = f32x16{}, dp0 = f32x16{}, s1 = f32x16{}, dp1 = f32x16{};
+        typename M::Row fq[3], fg[3];
+        typename M::Col cq[3], cg[3];
+        f32x4_t l4[4], d4[4];
+        // chunk n of both blocks' scores (sums) keeps its fragments in slot n % 3
+        auto load_rows = [&](int n) __attribute__((always_inline)) {
+          fq[n % 3] = Tl::row(qs, n / SR, n % SR, lane);
+          fg[n % 3] = Tl::row(gs, n / SR, n % SR, lane);
+        };
+        auto load_cols = [&](int n) __attribute__((always_inline)) {
+          cg[n % 3] = Tl::col(gs, n / C2, n % C2 / DB, n % DB, lane);
+          cq[n % 3] = Tl::col(qs, n / C2, n % C2 / DB, n % DB, lane);
+        };
+        auto load_stats = [&](int b, int r4) __attribute__((always_inline)) {
+          l4[r4] = *reinterpret_cast<const f32x4_t*>(&sc.lse2[32 * b + 8 * r4 + 4 * half]);
+          d4[r4] = *reinterpret_cast<const f32x4_t*>(&sc.delta[32 * b + 8 * r4 + 4 * half]);
+        };
+        auto weigh = [&](f32x16& s, f32x16& dp, int r) __attribute__((always_inline)) {
+          s[r] = exp2_hw(fmaf(s[r], a.scale_log2, -l4[r / 4][r % 4]));
+          dp[r] = s[r] * (dp[r] - d4[r / 4][r % 4]);
+        };
+        load_rows(0);
+        load_rows(1);
+#pragma unroll
+        for (int n = 0; n < 2 * SR; ++n) {              // scores; block 1's over the exponentials of block 0
+          const int c = n % SR;
+          if (n + 2 < 2 * SR) load_rows(n + 2);
+          else load_cols(n + 2 - 2 * SR);
+          if (n == SR - 2) { load_stats(0, 0); load_stats(0, 1); }
+          if (n == SR - 1) { load_stats(0, 2); load_stats(0, 3); }
+          f32x16 &s = n < SR ? s0 : s1, &dp = n < SR ? dp0 : dp1;
+          s = M::rows(fq[n % 3], kf[c], s);
+          dp = M::rows(fg[n % 3], vf[c], dp);
+          if (n >= SR) {
+#pragma unroll
+            for (int r = c * 16 / SR; r < (c + 1) * 16 / SR; ++r) weigh(s0, dp0, r);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) load_stats(1, r4);
+        typename M::Col p, ds;
+#pragma unroll
+        for (int n = 0; n < 2 * C2; ++n) {              // sums; block 0's over the exponentials of block 1
+          const int i = n % C2, d = n % DB;
+          if (d == 0) { p = M::regs(n < C2 ? s0 : s1, i / DB); ds = M::regs(n < C2 ? dp0 : dp1, i / DB); }
+          if (n + 2 < 2 * C2) load_cols(n + 2);
+          dv[d] = M::cols(cg[n % 3], p, dv[d]);
+          dk[d] = M::cols(cq[n % 3], ds, dk[d]);
+          if (n < C2) {
+#pragma unroll
+            for (int r = i * 16 / C2; r < (i + 1) * 16 / C2; ++r) weigh(s1, dp1, r);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+          f32x16 s, dp;
+          scores(b, s, dp);
+          weights(b, s, dp);
+          sums(b, s, dp);
+        }
       }
     }
-    if (more) put(sn, lse2n, deltan, limitn);
+    if (more) put(sn, r0 + RT, lsen, deltan);
   };
 
   if (it.lo < it.hi) {
     fetch(q0s, g0s, it.lo);
-    float lse2, delta;
-    int limit;
-    stats(it.lo, lse2, delta, limit);
-    put(st0, lse2, delta, limit);
-    for (int r = it.lo; r < it.hi; r += 2 * RT) {
-      step(q0s, g0s, st0, q1s, g1s, st1, r);
-      if (r + RT < it.hi) step(q1s, g1s, st1, q0s, g0s, st0, r + RT);
+    float lse, delta;
+    stats(it.lo, lse, delta);
+    put(st0, it.lo, lse, delta);
+    // rows at or past `whole` see all of the workgroup's keys: masked tiles
+    // first, in pairs, then the rest
+    const int whole = a.causal ? min((it.at + 32 * NW - 1 - off) * a.group, it.hi) : it.lo;
+    int r = it.lo;
+    for (; r < whole && r + RT < it.hi; r += 2 * RT) {
+      step(std::true_type{}, q0s, g0s, st0, q1s, g1s, st1, r);
+      step(std::true_type{}, q1s, g1s, st1, q0s, g0s, st0, r + RT);
     }
+    for (; r + RT < it.hi; r += 2 * RT) {
+      step(std::false_type{}, q0s, g0s, st0, q1s, g1s, st1, r);
+      step(std::false_type{}, q1s, g1s, st1, q0s, g0s, st0, r + RT);
+    }
+    if (r < it.hi) step(std::true_type{}, q0s, g0s, st0, q1s, g1s, st1, r);
   }
   if (it.part >= 0) {
     const int64_t slot = ((int64_t)it.part * a.kv_heads + kvh) * (32 * NW) + wave * 32 + l32;
@@ -317,33 +415,44 @@ __global__ __launch_bounds__(64 * NW, DP * T::kSize > 128 ? 1 : 2) void attn_dkv
   }
 }
 
-// Adds the parts of a split tile in order.  ROWS: dq (tile rows are query
-// rows); otherwise dk and dv (tile rows are keys).
+// Adds the parts of a split tile.  ROWS: dq (tile rows are query rows);
+// otherwise dk and dv (tile rows are keys).  A workgroup takes one tile row:
+// DP / 4 threads hold four channels each, 1024 / DP of them add every so-many-th
+// part, then their sums in order.
 template <class T, int DP, bool ROWS>
 __global__ __launch_bounds__(256) void attn_add(const AttnArgs a, int tile) {
-  const int kvh = blockIdx.x % a.kv_heads;
-  const AttnJoin j = a.joins[blockIdx.x / a.kv_heads];
-  for (int i = threadIdx.x; i < tile * (DP / 4); i += 256) {
-    const int r = i / (DP / 4), c = i % (DP / 4) * 4, at = j.at + r;
-    const int token = ROWS ? (int)quo(at, a.by_group) : at;
-    if (token >= (ROWS ? j.lq : j.lk) || c >= a.dim) continue;
-    f32x4_t x = f32x4_t{}, y = f32x4_t{};
+  constexpr int CT = DP / 4, LANES = 256 / CT;
+  __shared__ f32x4_t acc[ROWS ? 1 : 2][LANES][CT];
+  const int r = blockIdx.x % tile, unit = blockIdx.x / tile;
+  const int kvh = unit % a.kv_heads;
+  const AttnJoin j = a.joins[unit / a.kv_heads];
+  const int at = j.at + r, token = ROWS ? (int)quo(at, a.by_group) : at;
+  if (token >= (ROWS ? j.lq : j.lk)) return;
+  const int ct = threadIdx.x % CT, g = threadIdx.x / CT, c = 4 * ct;
+  f32x4_t x = f32x4_t{}, y = f32x4_t{};
+  if (g < LANES) {
 #pragma unroll 4
-    for (int p = 0; p < j.count; ++p) {
+    for (int p = g; p < j.count; p += LANES) {
       const int64_t e = (((int64_t)(j.first + p) * a.kv_heads + kvh) * tile + r) * DP + c;
       x += *reinterpret_cast<const f32x4_t*>(a.part + e);
       if constexpr (!ROWS) y += *reinterpret_cast<const f32x4_t*>(a.part2 + e);
     }
-    const float xv[4] = {x.x, x.y, x.z, x.w};
-    if constexpr (ROWS) {
-      const int head = kvh * a.group + at - token * a.group;
-      store_vec<T, 4>(a.dq.p + (int64_t)(j.q0 + token) * a.dq.t + (int64_t)head * a.dq.h + c * T::kSize, xv);
-    } else {
-      const float yv[4] = {y.x, y.y, y.z, y.w};
-      store_vec<T, 4>(a.dk.p + (int64_t)(j.k0 + at) * a.dk.t + (int64_t)kvh * a.dk.h + c * T::kSize, xv);
-      store_vec<T, 4>(a.dv.p + (int64_t)(j.k0 + at) * a.dv.t + (int64_t)kvh * a.dv.h + c * T::kSize, yv);
-    }
+    acc[0][g][ct] = x;
+    if constexpr (!ROWS) acc[1][g][ct] = y;
   }
+  __syncthreads();
+  const int n = min(LANES, j.count);
+  const bool second = !ROWS && threadIdx.x >= 64;       // dv by another wave
+  const int t = threadIdx.x - (second ? 64 : 0);
+  if (t >= CT || 4 * t >= a.dim || (second && threadIdx.x >= 128)) return;
+  x = f32x4_t{};
+  for (int i = 0; i < n; ++i) x += acc[ROWS ? 0 : second][i][t];
+  const float v[4] = {x.x, x.y, x.z, x.w};
+  char* p;
+  if constexpr (ROWS) p = a.dq.p + (int64_t)(j.q0 + token) * a.dq.t + (int64_t)(kvh * a.group + at - token * a.group) * a.dq.h;
+  else if (second) p = a.dv.p + (int64_t)(j.k0 + at) * a.dv.t + (int64_t)kvh * a.dv.h;
+  else p = a.dk.p + (int64_t)(j.k0 + at) * a.dk.t + (int64_t)kvh * a.dk.h;
+  store_vec<T, 4>(p + 4 * t * T::kSize, v);
 }
 
 template <class T, int DP> st_status backward_dim(st_seqs* s, AttnArgs a, hipStream_t st) {
@@ -368,7 +477,7 @@ template <class T, int DP> st_status backward_dim(st_seqs* s, AttnArgs a, hipStr
       st_status r = launch_check(rows ? "attn_dq" : "attn_dkv");
       if (r != ST_OK) return r;
       if (l.join[w].empty()) continue;
-      const int jg = (int)(l.join[w].size() * s->kv_heads);
+      const int jg = (int)(l.join[w].size() * s->kv_heads * tile);
       if (rows) attn_add<T, DP, true><<<jg, 256, 0, st>>>(a, tile);
       else attn_add<T, DP, false><<<jg, 256, 0, st>>>(a, tile);
       r = launch_check("attn_add");
@@ -404,7 +513,7 @@ extern "C" st_status st_attention_packed_backward(st_seqs* seqs, const st_tokens
   auto err = [](st_status s, const std::string& m) { return fail(s, "st_attention_packed_backward: " + m); };
   if (!seqs || !q || !k || !v || !out || !dout || !dq || !dk || !dv) return err(ST_ERR_INVALID_ARG, "NULL argument");
   if (!(scale > 0.f) || !std::isfinite(scale)) return err(ST_ERR_INVALID_ARG, "scale must be positive and finite");
-  const int es = seqs->dtype == ST_F32 ? 4 : 2, span = 64;
+  const int es = seqs->dtype == ST_F32 ? 4 : 2, span = 256;               // rows of the largest tile
   const int64_t tq = seqs->total_q, tk = seqs->total_k;
   AttnArgs a{};
   struct { AttnTensor* t; const st_tokens* v; bool keys; const char* name; } const all[] = {

@@ -17,7 +17,6 @@ namespace st {
 AttnShape attn_shape(st_dtype dtype, int dp) {
   AttnShape s{};
   const bool f32 = dtype == ST_F32;
-  (void)dp;
   s.tile[kListForward][0] = 128;
   s.tile[kListDq][0] = 128;
   s.tile[kListDkv][0] = 128;
