@@ -43,8 +43,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t attn_rsrc(const void* base, in
 // LDS chunk permutation of a tile row, by the row's pitch in bytes
 template <int PITCH> __device__ __forceinline__ constexpr int swizzle(int r) {
   return PITCH == 64 || PITCH == 192    ? (r >> 2) & 3
-         : PITCH == 128 || PITCH == 384 ? r & 7
-                                        : ((r & 3) << 1) | ((r >> 2) & 1);
+         : PITCH == 128 || PITCH == 384 ? (((r >> 1) & 1) << 2) | ((r >> 2) & 3)
+                                        : ((r & 3) << 2) | ((r >> 2) & 3);
 }
 
 // max, sum over the two halves of a wave (the two lanes of one column): the

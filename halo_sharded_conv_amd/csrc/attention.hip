@@ -34,11 +34,15 @@ template <class T> struct Special;
 template <> struct Special<BF16> {
   typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
   static __device__ __forceinline__ bool any(bf16x8 v) {
-    const u32x4_t w = __builtin_bit_cast(u32x4_t, v);
-    bool f = false;
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    const u32x4_t w = __builtin_bit_cast(u32x4_t, v) & 0x7FFF7FFFu;
+    u16x2 m = u16x2{0, 0};                              // largest magnitude of the even and odd values
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f |= ((w[i] & 0x7F80u) == 0x7F80u) | ((w[i] & 0x7F800000u) == 0x7F800000u);
-    return f;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t word = w[i];                       // (a bit cast of a vector's element reads element 0)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, word));
+    }
+    return (m.x >= 0x7F80) | (m.y >= 0x7F80);
   }
   static __device__ __forceinline__ bf16x8 finite(bf16x8 v) {
     u16x8 w = __builtin_bit_cast(u16x8, v);
@@ -83,8 +87,11 @@ __device__ __forceinline__ void special_sum(const char* v, int64_t stride, int j
   for (int i = 0; i < 4; ++i) x[i] = y[i];
 }
 
+// waves per SIMD that the registers allow
+template <class T, int DP> constexpr int fwd_waves() { return DP * T::kSize > 256 ? 1 : DP * T::kSize > 128 ? 2 : 3; }
+
 template <class T, int DP, int KT, int NW>
-__global__ __launch_bounds__(64 * NW, DP * T::kSize > 256 ? 1 : 2) void attn_forward(const AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, (fwd_waves<T, DP>())) void attn_forward(const AttnArgs a) {
   using M = Mma<T>;
   using Tl = Tile<T, DP, KT, NW>;
   constexpr int KB = KT / 32, SR = Tl::SR, DB = Tl::DB, NI = Tl::NI;
@@ -208,8 +215,9 @@ __global__ __launch_bounds__(64 * NW, DP * T::kSize > 256 ? 1 : 2) void attn_for
         for (int d = 0; d < DB; ++d) {
           typename M::Col w = Tl::col(vs, b, t, d, lane);
           if constexpr (masked) {
-            sp |= Special<T>::any(w);
-            w = Special<T>::finite(w);
+            const bool bad = Special<T>::any(w);
+            sp |= bad;
+            if (__any(bad)) w = Special<T>::finite(w);
           }
           o[d] = M::cols(w, p, o[d]);
         }

@@ -25,8 +25,11 @@ namespace {
 
 // ---------------------------------------------------------------------- dq
 
+// waves per SIMD that the registers allow
+template <class T, int DP> constexpr int dq_waves() { return DP * T::kSize > 256 ? 1 : DP * T::kSize > 128 ? 2 : 3; }
+
 template <class T, int DP, int KT, int NW>
-__global__ __launch_bounds__(64 * NW, DP * T::kSize > 256 ? 1 : 2) void attn_dq(const AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, (dq_waves<T, DP>())) void attn_dq(const AttnArgs a) {
   using M = Mma<T>;
   using Tl = Tile<T, DP, KT, NW>;
   constexpr int KB = KT / 32, SR = Tl::SR, DB = Tl::DB, NI = Tl::NI;
