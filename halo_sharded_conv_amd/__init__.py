@@ -249,9 +249,19 @@ def _torch():
     return torch
 
 
+def _current_stream() -> int:
+    """Handle of the current device's current stream, without building a
+    torch.cuda.Stream object (4 us of a 12 us call)."""
+    torch = _torch()
+    try:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    except AttributeError:                   # a torch without these two
+        return torch.cuda.current_stream().cuda_stream
+
+
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(_torch().cuda.current_stream().cuda_stream)
+        return ctypes.c_void_p(_current_stream())
     if hasattr(stream, "cuda_stream"):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -264,9 +274,8 @@ def _dev_ptr(t, what: str, min_bytes: int = 0) -> int:
         raise ShardConvError(1, f"{what}: expected a GPU tensor (no CPU fallback exists)")
     if not t.is_contiguous():
         raise ShardConvError(1, f"{what}: tensor must be contiguous")
-    nbytes = t.numel() * t.element_size()
-    if nbytes < min_bytes:
-        raise ShardConvError(2, f"{what}: tensor holds {nbytes} bytes, needs {min_bytes}")
+    if t.nbytes < min_bytes:
+        raise ShardConvError(2, f"{what}: tensor holds {t.nbytes} bytes, needs {min_bytes}")
     return t.data_ptr()
 
 
@@ -275,7 +284,10 @@ def _ptr_array(tensors, what: str, sizes: List[int]):
         raise ShardConvError(2, f"{what}: expected {len(sizes)} shard buffers, got {len(tensors)}")
     arr = (ctypes.c_void_p * max(1, len(tensors)))()
     for i, t in enumerate(tensors):
-        arr[i] = _dev_ptr(t, f"{what}[{i}]", sizes[i])
+        if t is not None and getattr(t, "is_cuda", False) and t.is_contiguous() and t.nbytes >= sizes[i]:
+            arr[i] = t.data_ptr()
+        else:
+            arr[i] = _dev_ptr(t, f"{what}[{i}]", sizes[i])   # its message
     return arr
 
 
@@ -531,7 +543,7 @@ def st_groupnorm_sharded_noalloc(y_plan: Plan, y_bufs, ymax, groups: int, eps: f
 
 def _ws(workspace):
     ws = _dev_ptr(workspace, "workspace")
-    return ws, (workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    return ws, (workspace.nbytes if workspace is not None else 0)
 
 
 def st_groupnorm_partials(y_plan: Plan, y_bufs, ymax, groups: int, workspace, stream=None) -> None:
@@ -664,14 +676,15 @@ def st_plan_positions(plan: Plan, pos_bufs, stream=None) -> None:
     _check(lib.st_plan_positions(plan.handle, ps, _stream(stream)), "st_plan_positions")
 
 
+_TENSOR_DTYPES = {_torch().float32: ST_F32, _torch().bfloat16: ST_BF16, _torch().int16: ST_BF16}
+
+
 def _float_dtype(t, what: str) -> int:
     """ST_F32 or ST_BF16 of a tensor (bf16 also as int16 bit patterns)."""
-    torch = _torch()
-    if t.dtype == torch.float32:
-        return ST_F32
-    if t.dtype in (torch.bfloat16, torch.int16):
-        return ST_BF16
-    raise ShardConvError(1, f"{what}: expected float32 or bfloat16, got {t.dtype}")
+    dt = _TENSOR_DTYPES.get(t.dtype)
+    if dt is None:
+        raise ShardConvError(1, f"{what}: expected float32 or bfloat16, got {t.dtype}")
+    return dt
 
 
 def _rows3(t, what: str):
@@ -721,6 +734,7 @@ class Sequences:
         self.total_q, self.total_k = sum(q_lens), sum(k_lens)
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         self.dtype, self.causal = dtype, causal
+        self.q_shape, self.k_shape = (self.total_q, heads, head_dim), (self.total_k, kv_heads, head_dim)
 
     @property
     def handle(self) -> ctypes.c_void_p:
@@ -769,13 +783,16 @@ def st_attention_workspace_bytes(seqs: Sequences, backward: bool = False) -> int
 
 
 def _tokens(t, what: str, seqs: Sequences, keys: bool) -> _Tokens:
-    _rows3(t, what)
-    want = (seqs.total_k if keys else seqs.total_q, seqs.kv_heads if keys else seqs.heads, seqs.head_dim)
-    if tuple(t.shape) != want:
+    want = seqs.k_shape if keys else seqs.q_shape
+    if t.shape != want or not t.is_cuda:
+        _rows3(t, what)
         raise ShardConvError(2, f"{what}: expected {want}, got {tuple(t.shape)}")
-    if _float_dtype(t, what) != seqs.dtype:
+    if _TENSOR_DTYPES.get(t.dtype) != seqs.dtype:
         raise ShardConvError(1, f"{what}: dtype {t.dtype} is not the plan's")
-    return _Tokens(t.data_ptr(), t.stride(0), t.stride(1))
+    st, sh, sc = t.stride()
+    if sc != 1:
+        _rows3(t, what)
+    return _Tokens(t.data_ptr(), st, sh)
 
 
 def st_attention_packed(seqs: Sequences, q, k, v, scale: float, out, lse=None, workspace=None, stream=None) -> None:
@@ -783,21 +800,26 @@ def st_attention_packed(seqs: Sequences, q, k, v, scale: float, out, lse=None, w
     head_dim]; any strides that are multiples of 16 bytes; lse: float32
     [total queries, heads] or None."""
     what = "st_attention_packed"
-    args = [_tokens(t, f"{what} {n}", seqs, n in "kv") for n, t in (("q", q), ("k", k), ("v", v), ("out", out))]
-    l = _dev_ptr(lse, f"{what} lse", 4 * seqs.total_q * seqs.heads)
+    l = _dev_ptr(lse, "st_attention_packed lse", 4 * seqs.total_q * seqs.heads)
     ws, nb = _ws(workspace)
-    _check(lib.st_attention_packed(seqs.handle, args[0], args[1], args[2], float(scale), args[3], l, ws, nb,
-                                   _stream(stream)), what)
+    _check(lib.st_attention_packed(seqs.handle, _tokens(q, "st_attention_packed q", seqs, False),
+                                   _tokens(k, "st_attention_packed k", seqs, True),
+                                   _tokens(v, "st_attention_packed v", seqs, True), scale,
+                                   _tokens(out, "st_attention_packed out", seqs, False), l, ws, nb, _stream(stream)), what)
 
 
 def st_attention_packed_backward(seqs: Sequences, q, k, v, out, lse, dout, scale: float, dq, dk, dv, workspace,
                                  stream=None) -> None:
     """dq, dk, dv of st_attention_packed; out and lse as it wrote them."""
+    def view(t, n, keys):
+        return _tokens(t, n, seqs, keys)
+
     what = "st_attention_packed_backward"
-    args = [_tokens(t, f"{what} {n}", seqs, keys) for n, t, keys in
-            (("q", q, False), ("k", k, True), ("v", v, True), ("out", out, False), ("dout", dout, False),
-             ("dq", dq, False), ("dk", dk, True), ("dv", dv, True))]
-    l = _dev_ptr(lse, f"{what} lse", 4 * seqs.total_q * seqs.heads)
+    l = _dev_ptr(lse, "st_attention_packed_backward lse", 4 * seqs.total_q * seqs.heads)
     ws, nb = _ws(workspace)
-    _check(lib.st_attention_packed_backward(seqs.handle, args[0], args[1], args[2], args[3], l, args[4], float(scale),
-                                            args[5], args[6], args[7], ws, nb, _stream(stream)), what)
+    _check(lib.st_attention_packed_backward(
+        seqs.handle, view(q, "st_attention_packed_backward q", False), view(k, "st_attention_packed_backward k", True),
+        view(v, "st_attention_packed_backward v", True), view(out, "st_attention_packed_backward out", False), l,
+        view(dout, "st_attention_packed_backward dout", False), scale, view(dq, "st_attention_packed_backward dq", False),
+        view(dk, "st_attention_packed_backward dk", True), view(dv, "st_attention_packed_backward dv", True), ws, nb,
+        _stream(stream)), what)
