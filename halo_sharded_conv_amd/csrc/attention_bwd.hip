@@ -165,6 +165,18 @@ __global__ __launch_bounds__(64 * NW, (dq_waves<T, DP>())) void attn_dq(const At
 
 // ------------------------------------------------------------------ dk, dv
 
+// The lane index of a step.  The fp32 col fragments of a wide head have 64
+// different LDS addresses: FRESH forms them in each step, a few instructions
+// under long products, where held over the loop they spill (8 heads of 128,
+// 4096 tokens: 2524 -> 1104 us).  Everywhere else the compiler's choice to hold
+// them is 5 to 13% faster.
+template <bool FRESH> struct LaneOf {
+  static __device__ __forceinline__ int of(int lane) {
+    if constexpr (FRESH) asm volatile("" : "+v"(lane));
+    return lane;
+  }
+};
+
 // waves per SIMD that the registers allow: K, V and the sums of dk and dv
 template <class T, int DP> constexpr int dkv_waves() { return DP * T::kSize > 128 ? 1 : 2; }
 
@@ -175,11 +187,15 @@ void attn_dkv(const AttnArgs a) {
   using Tl = Tile<T, DP, RT, NW>;
   constexpr int RB = RT / 32, SR = Tl::SR, DB = Tl::DB, NI = Tl::NI;
   constexpr bool PIPE = T::kSize == 2 && RB == 2 && dkv_waves<T, DP>() == 1;
+  // wide fp32 heads: V in LDS beside the tiles, its registers for the sums
+  using Tv = Tile<T, DP, 32 * NW, NW>;
+  constexpr bool VL = T::kSize == 4 && DP > 64;
   struct Stats { float lse2[RT], delta[RT]; int limit[RT]; };
   __shared__ __attribute__((aligned(1024))) char q0s[Tl::BYTES];
   __shared__ __attribute__((aligned(1024))) char g0s[Tl::BYTES];
   __shared__ __attribute__((aligned(1024))) char q1s[Tl::BYTES];
   __shared__ __attribute__((aligned(1024))) char g1s[Tl::BYTES];
+  __shared__ __attribute__((aligned(1024))) char vls[VL ? Tv::BYTES : 16];
   __shared__ __attribute__((aligned(16))) Stats st0, st1;
   const int tid = threadIdx.x;
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -190,7 +206,7 @@ void attn_dkv(const AttnArgs a) {
   const int key0 = it.at + wave * 32, key = key0 + l32;
   const bool live = key < it.lk;
 
-  typename M::Row kf[SR], vf[SR];
+  typename M::Row kf[SR], vf[VL ? 1 : SR];
   {
     const char* pk = a.k.p + (int64_t)(it.k0 + key) * a.k.t + (int64_t)kvh * a.k.h;
     const char* pv = a.v.p + (int64_t)(it.k0 + key) * a.v.t + (int64_t)kvh * a.v.h;
@@ -199,7 +215,17 @@ void attn_dkv(const AttnArgs a) {
       const int byte = (2 * s + half) * 16;
       const bool in = live && byte < a.dim * T::kSize;
       kf[s] = in ? *reinterpret_cast<const typename M::Row*>(pk + byte) : typename M::Row{};
-      vf[s] = in ? *reinterpret_cast<const typename M::Row*>(pv + byte) : typename M::Row{};
+      if constexpr (!VL) vf[s] = in ? *reinterpret_cast<const typename M::Row*>(pv + byte) : typename M::Row{};
+    }
+  }
+  if (VL && it.lo < it.hi) {                            // (in LDS before the first tile is read: step's wait and barrier)
+    const int64_t left = min(32 * NW, it.lk - it.at);
+    const auto rv = attn_rsrc(a.v.p + (int64_t)(it.k0 + it.at) * a.v.t + (int64_t)kvh * a.v.h, left * a.v.t);
+#pragma unroll
+    for (int i = 0; i < Tv::NI; ++i) {
+      const int r = Tv::dma_row(wave, lane, i), b = Tv::dma_byte(wave, lane, i);
+      const uint32_t at = b < a.dim * T::kSize ? (uint32_t)(r * (int)a.v.t + b) : kOobOffset;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_void)Tv::dma_dst(vls, wave, i), 16, at, 0, 0, 0);
     }
   }
   f32x16 dk[DB], dv[DB];
@@ -262,6 +288,7 @@ void attn_dkv(const AttnArgs a) {
     __builtin_amdgcn_s_waitcnt(0x0F70);
     __syncthreads();
     const bool more = r0 + RT < it.hi;
+    const int ln = LaneOf<VL>::of(lane);
     float lsen, deltan;
     if (more) {
       fetch(qn, gn, r0 + RT);
@@ -275,8 +302,10 @@ void attn_dkv(const AttnArgs a) {
         dp = f32x16{};
 #pragma unroll
         for (int c = 0; c < SR; ++c) {
-          s = M::rows(Tl::row(qs, b, c, lane), kf[c], s);
-          dp = M::rows(Tl::row(gs, b, c, lane), vf[c], dp);
+          s = M::rows(Tl::row(qs, b, c, ln), kf[c], s);
+          if constexpr (VL) dp = M::rows(Tl::row(gs, b, c, ln), Tv::row(vls, wave, c, ln), dp);
+          else dp = M::rows(Tl::row(gs, b, c, ln), vf[c], dp);
+          if constexpr (VL) __builtin_amdgcn_sched_barrier(0);   // no reads hoisted into registers that are not there
         }
       };
       auto weights = [&](int b, f32x16& s, f32x16& dp) __attribute__((always_inline)) {   // s -> p, dp -> ds
@@ -301,8 +330,9 @@ void attn_dkv(const AttnArgs a) {
           const typename M::Col p = M::regs(s, t), ds = M::regs(dp, t);
 #pragma unroll
           for (int d = 0; d < DB; ++d) {
-            dv[d] = M::cols(Tl::col(gs, b, t, d, lane), p, dv[d]);
-            dk[d] = M::cols(Tl::col(qs, b, t, d, lane), ds, dk[d]);
+            dv[d] = M::cols(Tl::col(gs, b, t, d, ln), p, dv[d]);
+            dk[d] = M::cols(Tl::col(qs, b, t, d, ln), ds, dk[d]);
+            if constexpr (VL) __builtin_amdgcn_sched_barrier(0);
           }
         }
       };
@@ -318,12 +348,12 @@ void attn_dkv(const AttnArgs a) {
         f32x4_t l4[4], d4[4];
         // chunk n of both blocks' scores (sums) keeps its fragments in slot n % 3
         auto load_rows = [&](int n) __attribute__((always_inline)) {
-          fq[n % 3] = Tl::row(qs, n / SR, n % SR, lane);
-          fg[n % 3] = Tl::row(gs, n / SR, n % SR, lane);
+          fq[n % 3] = Tl::row(qs, n / SR, n % SR, ln);
+          fg[n % 3] = Tl::row(gs, n / SR, n % SR, ln);
         };
         auto load_cols = [&](int n) __attribute__((always_inline)) {
-          cg[n % 3] = Tl::col(gs, n / C2, n % C2 / DB, n % DB, lane);
-          cq[n % 3] = Tl::col(qs, n / C2, n % C2 / DB, n % DB, lane);
+          cg[n % 3] = Tl::col(gs, n / C2, n % C2 / DB, n % DB, ln);
+          cq[n % 3] = Tl::col(qs, n / C2, n % C2 / DB, n % DB, ln);
         };
         auto load_stats = [&](int b, int r4) __attribute__((always_inline)) {
           l4[r4] = *reinterpret_cast<const f32x4_t*>(&sc.lse2[32 * b + 8 * r4 + 4 * half]);
