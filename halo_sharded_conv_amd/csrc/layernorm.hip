@@ -30,7 +30,9 @@ namespace {
 
 constexpr int kLnThreads = 256;
 constexpr int kLnMaxC = 16384;
-constexpr int kLnMaxParts = 1024;     // workgroups (partial rows) of the backward pass
+// workgroups (partial rows) of the backward pass: four a CU (2048: the partial
+// rows' sums take 8 us in place of 5, the pass is no faster)
+constexpr int kLnMaxParts = 1024;
 
 struct LnTensor {                     // one tensor's view of a shard's interior
   char* p;                            // first interior cell
@@ -64,13 +66,31 @@ __device__ __forceinline__ int64_t cell_of(const LnShard& s, int t, bool flat, u
   return (int64_t)n * s.t[t].sn + (int64_t)d * s.t[t].sd + (int64_t)h * s.t[t].sh + w;
 }
 
-// sum over the lanes of one cell
+// v plus the value of the lane that DPP control C names
+template <int C> __device__ __forceinline__ float add_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), C, 0xF, 0xF, false));
+}
+
+// sum over the lanes of one cell (a power of two of them): within 16 lanes by
+// DPP (pairs, quads, then mirrors, whose partners hold whole quads and halves),
+// beyond by lane swaps; no LDS round trips
 template <bool BLOCK> __device__ __forceinline__ float cell_sum(float v, int lpr, float* red) {
   const int n = BLOCK ? 64 : lpr;
-  for (int m = 1; m < n; m <<= 1) v += __shfl_xor(v, m);
+  if (n > 1) v = add_dpp<0xB1>(v);                      // quad_perm 1 0 3 2
+  if (n > 2) v = add_dpp<0x4E>(v);                      // quad_perm 2 3 0 1
+  if (n > 4) v = add_dpp<0x141>(v);                     // row_half_mirror
+  if (n > 8) v = add_dpp<0x140>(v);                     // row_mirror
+  if (n > 16) {
+    const u32x2_t r = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if (n > 32) {
+    const u32x2_t r = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
   if constexpr (BLOCK) {
     const int wave = threadIdx.x >> 6;
-    __syncthreads();                  // the last sum's readers are done
+    __syncthreads();                                    // the last sum's readers are done
     if ((threadIdx.x & 63) == 0) red[wave] = v;
     __syncthreads();
     v = (red[0] + red[1]) + (red[2] + red[3]);
@@ -78,7 +98,9 @@ template <bool BLOCK> __device__ __forceinline__ float cell_sum(float v, int lpr
   return v;
 }
 
-template <int VEC, int NV> constexpr int ln_unroll() { return NV * VEC >= 32 ? 1 : NV * VEC >= 16 ? 2 : 4; }
+// cells of one lane group in flight per pass, by the values a lane holds of one
+constexpr int ln_unroll(int per) { return per >= 32 ? 1 : per >= 16 ? 2 : 4; }
+constexpr int kLnBackUnroll = 2;      // (1: 373 us, 4: 340 us against 335 us on 2048^2 x 64 bf16; 4 is slower on fp32)
 
 __device__ __forceinline__ int shard_of(const LnArgs& a, int block) {
   int s = 0;
@@ -88,7 +110,7 @@ __device__ __forceinline__ int shard_of(const LnArgs& a, int block) {
 
 template <class TX, int VEC, int NV, bool BLOCK>
 __global__ __launch_bounds__(kLnThreads) void ln_forward(const LnArgs a) {
-  constexpr int U = BLOCK ? 1 : ln_unroll<VEC, NV>();
+  constexpr int U = BLOCK ? 1 : ln_unroll(NV * VEC);
   __shared__ float red[4];
   const int lpr = BLOCK ? kLnThreads : 1 << a.lpr_log2;
   const int sub = threadIdx.x & (lpr - 1), slot = threadIdx.x / lpr, rp = kLnThreads / lpr;
@@ -159,15 +181,15 @@ __global__ __launch_bounds__(kLnThreads) void ln_forward(const LnArgs a) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) y[i] = fmaf(x[u][k][i] * rstd[u], g[i], b[i]);
       const int64_t e = cell_of(s, 1, a.flat & 2, r) * C + c;
-      if (a.out_bf16) store_vec<BF16, VEC>(s.t[1].p + e * 2, y);
-      else store_vec<F32, VEC>(s.t[1].p + e * 4, y);
+      if (a.out_bf16) store_vec_nt<BF16, VEC>(s.t[1].p + e * 2, y);
+      else store_vec_nt<F32, VEC>(s.t[1].p + e * 4, y);
     }
   }
 }
 
 template <class TX, class TY, int VEC, int NV, bool BLOCK>
 __global__ __launch_bounds__(kLnThreads) void ln_backward(const LnArgs a) {
-  constexpr int U = BLOCK ? 1 : NV * VEC >= 16 ? 1 : 2;
+  constexpr int U = BLOCK ? 1 : kLnBackUnroll;
   __shared__ float red[4];
   const int lpr = BLOCK ? kLnThreads : 1 << a.lpr_log2;
   const int sub = threadIdx.x & (lpr - 1), slot = threadIdx.x / lpr, rp = kLnThreads / lpr;
@@ -235,8 +257,8 @@ __global__ __launch_bounds__(kLnThreads) void ln_backward(const LnArgs a) {
         float dx[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) dx[i] = rstd[u] * (dy[u][k][i] - s1 - x[u][k][i] * s2);
-        if (a.out_bf16) store_vec<BF16, VEC>(s.t[2].p + (cell + c) * 2, dx);
-        else store_vec<F32, VEC>(s.t[2].p + (cell + c) * 4, dx);
+        if (a.out_bf16) store_vec_nt<BF16, VEC>(s.t[2].p + (cell + c) * 2, dx);
+        else store_vec_nt<F32, VEC>(s.t[2].p + (cell + c) * 4, dx);
       }
     }
   }
@@ -328,10 +350,8 @@ LnPick ln_pick(int C, bool wide, bool backward) {
 }
 
 int ln_rows_per_block(const LnPick& p, bool backward) {
-  if (p.block) return 1;
   const int per = p.nv * p.vec;
-  const int u = backward ? (per >= 16 ? 1 : 2) : (per >= 32 ? 1 : per >= 16 ? 2 : 4);
-  return (kLnThreads >> p.lpr_log2) * u;
+  return p.block ? 1 : (kLnThreads >> p.lpr_log2) * (backward ? kLnBackUnroll : ln_unroll(per));
 }
 
 int64_t shard_rows(const st_plan* p, const Shard& s) { return p->batch * s.ext[0] * s.ext[1] * s.ext[2]; }
@@ -448,7 +468,9 @@ st_status st_layernorm_sharded(const st_plan* x_plan, const void* const* x_bufs,
   if (s != ST_OK) return s;
   s = ln_tensor(a, 1, y_plan, y_bufs, "st_layernorm_sharded: y");
   if (s != ST_OK) return s;
-  const bool wide = x_plan->dtype == ST_BF16 || y_plan->dtype == ST_BF16;
+  // 8 values a lane only where both sides are bf16: with an fp32 side, 4 keep its
+  // loads dense (1024 x 1792 x 256, fp32 to bf16: 471 -> 458 us)
+  const bool wide = x_plan->dtype == ST_BF16 && y_plan->dtype == ST_BF16;
   const LnPick pick = ln_pick((int)x_plan->channels, wide, false);
   s = ln_geometry(a, x_plan, pick, false);
   if (s != ST_OK) return s;
@@ -488,6 +510,8 @@ st_status st_layernorm_backward(const st_plan* x_plan, const void* const* x_bufs
   if (s != ST_OK) return s;
   s = ln_tensor(a, 2, dx_plan, dx_bufs, "st_layernorm_backward: dx");
   if (s != ST_OK) return s;
+  // 8 values a lane with any bf16 side: the same volume's backward pass takes
+  // 906 us with 8 and 1028 us with 4 (half as many bytes in flight)
   const bool wide = x_plan->dtype == ST_BF16 || dy_plan->dtype == ST_BF16 || dx_plan->dtype == ST_BF16;
   const LnPick pick = ln_pick((int)x_plan->channels, wide, true);
   s = ln_geometry(a, x_plan, pick, true);

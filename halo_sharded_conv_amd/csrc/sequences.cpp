@@ -24,12 +24,19 @@ AttnShape attn_shape(st_dtype dtype, int dp) {
   s.step[kListForward] = f32 ? 32 : 64;
   s.step[kListDq] = f32 ? 32 : 64;
   s.step[kListDkv] = f32 ? 32 : 64;
+  // Two four-wave or four one-wave workgroups per CU.  Also where a CU holds one
+  // (wide dk, dv; fp32): half as many, longer pieces leave the GPU uneven (a
+  // causal 8192-token step's dk and dv 690 -> 935 us), more pay for more partial
+  // results (mixed images forward 59 -> 98 us at 1024).
+  for (int l = 0; l < kLists; ++l) {
+    s.fill[l][0] = 512;
+    s.fill[l][1] = 1024;
+  }
   return s;
 }
 
 namespace {
 
-constexpr int64_t kTargetWgs[2] = {512, 1024};  // 2 four-wave or 4 one-wave workgroups per CU
 constexpr int kMinSteps = 4;                     // shortest split: 4 steps of the loop
 
 struct Seq {
@@ -70,7 +77,8 @@ void build(st_seqs* p, const std::vector<Seq>& seqs, int which) {
     }
   }
   for (int w = 0; w < 2; ++w) {
-    const int64_t per = std::max<int64_t>(kMinSteps, (steps[w] * p->kv_heads + kTargetWgs[w] - 1) / kTargetWgs[w]);
+    const int64_t fill = p->shape.fill[which][w];
+    const int64_t per = std::max<int64_t>(kMinSteps, (steps[w] * p->kv_heads + fill - 1) / fill);
     std::vector<AttnItem> out;
     out.reserve(l.item[w].size());
     for (const AttnItem& it : l.item[w]) {

@@ -39,6 +39,7 @@ enum { kListForward = 0, kListDq = 1, kListDkv = 2, kLists = 3 };
 struct AttnShape {
   int tile[kLists][2];      // rows (keys) per tile: four waves, one wave
   int step[kLists];         // keys (rows) of one step of the loop
+  int fill[kLists][2];      // workgroups that fill the GPU
 };
 inline int attn_padded_dim(int dim) { return dim <= 32 ? 32 : dim <= 64 ? 64 : dim <= 96 ? 96 : 128; }
 AttnShape attn_shape(st_dtype dtype, int padded_dim);

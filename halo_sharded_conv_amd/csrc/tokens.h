@@ -95,4 +95,29 @@ template <class T, int VEC> __device__ __forceinline__ void store_vec(char* p, c
   }
 }
 
+// the same past the caches' reach: for outputs that only a later pass reads
+template <class T, int VEC> __device__ __forceinline__ void store_vec_nt(char* p, const float (&x)[VEC]) {
+  if constexpr (T::kSize == 4) {
+    if constexpr (VEC % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < VEC / 4; ++i)
+        __builtin_nontemporal_store(f32x4_t{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]}, reinterpret_cast<f32x4_t*>(p) + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) __builtin_nontemporal_store(x[i], reinterpret_cast<float*>(p) + i);
+    }
+  } else {
+    if constexpr (VEC == 8) {
+      __builtin_nontemporal_store(u32x4_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                                               pack_bf16(x[6], x[7])}, reinterpret_cast<u32x4_t*>(p));
+    } else if constexpr (VEC == 4) {
+      __builtin_nontemporal_store(u32x2_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])}, reinterpret_cast<u32x2_t*>(p));
+    } else if constexpr (VEC == 2) {
+      __builtin_nontemporal_store(pack_bf16(x[0], x[1]), reinterpret_cast<uint32_t*>(p));
+    } else {
+      __builtin_nontemporal_store((uint16_t)pack_bf16(x[0], 0.f), reinterpret_cast<uint16_t*>(p));
+    }
+  }
+}
+
 }  // namespace st
