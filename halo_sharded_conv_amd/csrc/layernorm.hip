@@ -422,8 +422,10 @@ template <class TX> st_status ln_forward_launch(const LnArgs& a, const LnPick& p
   const dim3 grid(a.blocks), block(kLnThreads);
 #define LN_CASE(V, N, B) \
   if (p.vec == V && p.nv == N && p.block == B) { ln_forward<TX, V, N, B><<<grid, block, 0, st>>>(a); return launch_check("ln_forward"); }
-  LN_CASE(8, 1, false) LN_CASE(8, 2, false) LN_CASE(8, 4, false) LN_CASE(8, 8, false)
-  LN_CASE(8, 4, true) LN_CASE(8, 8, true)
+  if constexpr (TX::kSize == 2) {                       // (8 a lane: both sides bf16)
+    LN_CASE(8, 1, false) LN_CASE(8, 2, false) LN_CASE(8, 4, false) LN_CASE(8, 8, false)
+    LN_CASE(8, 4, true) LN_CASE(8, 8, true)
+  }
   LN_CASE(4, 1, false) LN_CASE(4, 2, false) LN_CASE(4, 4, false) LN_CASE(4, 8, false)
   LN_CASE(4, 4, true) LN_CASE(4, 8, true) LN_CASE(4, 16, true)
   LN_CASE(1, 1, false) LN_CASE(1, 4, false) LN_CASE(1, 16, false)

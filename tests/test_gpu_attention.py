@@ -277,6 +277,32 @@ def test_streams_and_graphs(gpu_lib):
         same()
 
 
+@pytest.mark.parametrize("q_lens,k_lens", [([5, 70], [0, 0]), ([0, 0], [40, 3]), ([3, 0], [0, 9])])
+def test_no_keys_or_no_queries(gpu_lib, q_lens, k_lens):
+    """Rows without a key give zeros and -inf, keys without a row zero gradients."""
+    for causal in (False, True):
+        host = inputs(q_lens, k_lens, 4, 2, 64, "bf16", seed=9)
+        r = run(gpu_lib, *[t.cuda() for t in host], q_lens, k_lens, "bf16", causal, 0.1)
+        assert all(bool((r[n] == 0).all()) for n in ("out", "dq", "dk", "dv")) and bool(torch.isneginf(r["lse"]).all())
+
+
+def test_offsets_past_32_bits(gpu_lib):
+    """Keys and values 128 KiB apart: the last lie 8.6 GB into their buffer."""
+    n, gap = 65600, 65536
+    rng = np.random.default_rng(10)
+    k, v = (torch.from_numpy(rng.normal(size=(n, 1, 64))).bfloat16().cuda() for _ in range(2))
+    q = torch.from_numpy(rng.normal(size=(3, 2, 64))).bfloat16().cuda()
+    big = torch.empty(n, 1, gap, dtype=torch.bfloat16, device="cuda")
+    kb, vb = big[:, :, :64], big[:, :, gap - 64:]
+    kb.copy_(k)
+    vb.copy_(v)
+    dout = torch.ones_like(q)
+    want = run(gpu_lib, q, k, v, dout, [3], [n], "bf16", True, 0.125)
+    got = run(gpu_lib, q, kb, vb, dout, [3], [n], "bf16", True, 0.125)
+    for name in ("out", "lse", "dq", "dk", "dv"):
+        assert torch.equal(got[name], want[name]), name
+
+
 def test_refusals_on_the_gpu(gpu_lib):
     seqs = gpu_lib.st_plan_sequences([8], None, 2, 2, 64, "bf16", False)
     t = torch.zeros(8, 2, 64, dtype=torch.bfloat16, device="cuda")

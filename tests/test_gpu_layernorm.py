@@ -221,6 +221,24 @@ def test_gradient_against_differences(gpu_lib):
         assert abs(got - want) <= 0.02 * float(torch.linalg.vector_norm(r[name].double())), name
 
 
+def test_offsets_past_32_bits(gpu_lib):
+    """A shard of 2.2e9 values: its last cells are those of a small shard."""
+    n, c = 270000, 8200
+    x = torch.empty(n, c, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    g = torch.randn(c, device="cuda")
+
+    def both(rows):
+        m = len(rows)
+        plan = gpu_lib.st_plan_shards(2, 1, c, (1, m), ((1,), (m,)), (0, 0), "bf16")
+        y, dx, stats = torch.empty_like(rows), torch.empty_like(rows), torch.empty(m, 2, device="cuda")
+        gpu_lib.st_layernorm_sharded(plan, [rows], g, None, 1e-5, plan, [y], stats)
+        ws = torch.empty(gpu_lib.st_layernorm_backward_workspace_bytes(plan), dtype=torch.uint8, device="cuda")
+        gpu_lib.st_layernorm_backward(plan, [rows], plan, [y], g, stats, plan, [dx], None, None, ws)
+        return y[-40:].clone(), dx[-40:].clone(), stats[-40:].clone()
+
+    assert all(torch.equal(a, b) for a, b in zip(both(x), both(x[-40:].clone())))
+
+
 def test_refusals_on_the_gpu(gpu_lib):
     s = Shards(gpu_lib, (4, 9), ((4,), (9,)), 1, 64, 0, "f32", margin=0.0)
     o = Shards(gpu_lib, (4, 9), ((3, 1), (9,)), 1, 64, 0, "f32", margin=0.0)

@@ -75,6 +75,17 @@ def test_views(gpu_lib):
     assert bool((ob[:, :, 64:] == 3.0).all())
 
 
+def test_offsets_past_32_bits(gpu_lib):
+    """2.3e9 values: the last tokens are those of a small call."""
+    t = 140000
+    x = torch.empty(t, 64, 256, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    pos = torch.arange(2 * t, dtype=torch.int32, device="cuda").view(t, 2)
+    want = x[-30:].clone()
+    gpu_lib.st_rope_axes(want, pos[-30:].clone(), [128, 128], want)
+    gpu_lib.st_rope_axes(x, pos, [128, 128], x)
+    assert torch.equal(x[-30:], want)
+
+
 def test_special_values_outside_the_rotation(gpu_lib):
     """Copied channels and heads keep NaN, infinities and the sign of zero."""
     x = torch.randn(6, 3, 64, device="cuda")
