@@ -74,7 +74,6 @@ __global__ __launch_bounds__(64 * NW, (dq_waves<T, DP>())) void attn_dq(const At
   if (live) {
     lse2 = a.lse[stat] * kLog2e;
     if (lse2 == -INFINITY) lse2 = INFINITY;
-    if (half == 0 && it.lo == 0) a.delta[stat] = delta;   // the tile's first part writes it
   }
   uint32_t koff[NI], voff[NI];
 #pragma unroll
@@ -121,14 +120,25 @@ __global__ __launch_bounds__(64 * NW, (dq_waves<T, DP>())) void attn_dq(const At
         dp = M::rows(Tl::row(vs, b, c, lane), gf[c], dp);
       }
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        dp[r] = exp2_hw(fmaf(s[r], a.scale_log2, -lse2)) * (dp[r] - delta);
+      for (int r = 0; r < 16; ++r) s[r] = exp2_hw(fmaf(s[r], a.scale_log2, -lse2));
       if constexpr (masked) {
         const int lim = limit - j0 - 4 * half;
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          if (32 * b + 8 * (r / 4) + r % 4 >= lim) dp[r] = 0.f;
+          if (32 * b + 8 * (r / 4) + r % 4 >= lim) { s[r] = 0.f; dp[r] = 0.f; }
+        if (b == 0 && j0 == 0) {
+          // A row with all its keys in these 32 takes D as the sum of p dp in
+          // fp32: `out` is rounded to its type, and with few keys that rounding
+          // is as large as all others together.
+          float d = 0.f;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) d = fmaf(s[r], dp[r], d);
+          d = half_sum(d);
+          delta = limit <= 32 ? d : delta;
+        }
       }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) dp[r] = s[r] * (dp[r] - delta);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const typename M::Col p = M::regs(dp, t);
@@ -150,6 +160,7 @@ __global__ __launch_bounds__(64 * NW, (dq_waves<T, DP>())) void attn_dq(const At
       if (j + KT < it.hi) step(std::true_type{}, k1s, v1s, k0s, v0s, j + KT);
     }
   }
+  if (live && half == 0 && it.lo == 0) a.delta[stat] = delta;   // the tile's first part writes it
   if (it.part >= 0) {
     const int64_t slot = ((int64_t)it.part * a.kv_heads + kvh) * (32 * NW) + wave * 32 + l32;
 #pragma unroll
