@@ -119,13 +119,14 @@ __global__ __launch_bounds__(64 * NW, (dq_waves<T, DP>())) void attn_dq(const At
         s = M::rows(Tl::row(ks, b, c, lane), qf[c], s);
         dp = M::rows(Tl::row(vs, b, c, lane), gf[c], dp);
       }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] = exp2_hw(fmaf(s[r], a.scale_log2, -lse2));
       if constexpr (masked) {
         const int lim = limit - j0 - 4 * half;
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (32 * b + 8 * (r / 4) + r % 4 >= lim) { s[r] = 0.f; dp[r] = 0.f; }
+        for (int r = 0; r < 16; ++r) {
+          const bool seen = 32 * b + 8 * (r / 4) + r % 4 < lim;
+          s[r] = seen ? exp2_hw(fmaf(s[r], a.scale_log2, -lse2)) : 0.f;
+          dp[r] = seen ? dp[r] : 0.f;
+        }
         if (b == 0 && j0 == 0) {
           // A row with all its keys in these 32 takes D as the sum of p dp in
           // fp32: `out` is rounded to its type, and with few keys that rounding
@@ -136,9 +137,13 @@ __global__ __launch_bounds__(64 * NW, (dq_waves<T, DP>())) void attn_dq(const At
           d = half_sum(d);
           delta = limit <= 32 ? d : delta;
         }
-      }
+        __builtin_amdgcn_sched_barrier(0);              // (few tiles: registers before speed)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) dp[r] = s[r] * (dp[r] - delta);
+        for (int r = 0; r < 16; ++r) dp[r] = s[r] * (dp[r] - delta);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dp[r] = exp2_hw(fmaf(s[r], a.scale_log2, -lse2)) * (dp[r] - delta);
+      }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const typename M::Col p = M::regs(dp, t);
