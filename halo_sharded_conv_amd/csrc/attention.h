@@ -13,9 +13,11 @@
 // step t; which tile row a slot stands for is free as long as the col fragment
 // uses the same one, so no lane ever exchanges scores with another.
 //
-// 16-byte chunk c of tile row r sits at chunk c ^ swizzle(r): eight lanes that
-// read one chunk of eight successive rows, and sixteen lanes that read 32 bytes
-// of four successive rows, then touch every bank once.
+// 16-byte chunk c of tile row r sits at chunk c ^ swizzle(r).  LDS serves 256
+// bytes a clock, sixteen lanes of a 16-byte read or thirty-two of an 8-byte one:
+// sixteen lanes that read one chunk of sixteen successive rows, and two groups of
+// sixteen that each read 32 bytes of four successive rows, then touch every bank
+// once (no conflict counted in any kernel here).
 #pragma once
 
 #include "sequences.h"

@@ -14,6 +14,17 @@
 // Rows are (token, head of the group) pairs, so heads that share keys share
 // the tiles of K and V, and a single query token of a grouped head still fills
 // the rows of a tile.
+//
+// Bound: the matrix cores, with the exponentials beside them (64 channels: as
+// long as the products).  Tile: 4 waves of 32 rows share 64 keys of K and V, two
+// stages; K Q^T reads a tile once per 32 rows, which leaves the LDS a quarter
+// busy.  Three waves per SIMD up to 128 bytes a row (64 channels: 912 -> 971
+// TFLOP/s), two above.  Measured: 4 x 4096 tokens, 16 heads of 128: 520 us, 1050
+// TFLOP/s (76% of a large bf16 product); causal 16001 tokens, 16 / 4 heads of
+// 128: 1.0 ms, 1030; 2 x 8192, 16 heads of 64: 575 us, 950; fp32, 4096 tokens, 8
+// heads of 128: 580 us, 118 (77% of a large fp32 product).  One wave with 32 keys
+// a step serves sequences of up to 64 rows: single tokens of 16 / 4 heads of 64
+// over 79000 keys 24 us, 5.0 TB/s.
 #include <algorithm>
 #include <cmath>
 #include <string>

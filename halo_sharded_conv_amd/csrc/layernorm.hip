@@ -13,8 +13,11 @@
 // writes dx once; a cell stays in registers between its load and its store,
 // so the variance is the centred one (two passes over registers, none over
 // memory).  A cell is held by `lpr` lanes (a power of two, so sums cross
-// lanes by xor shuffles), or by the 256 threads of a workgroup when it is
-// wider than a wave holds.  All sums and statistics are fp32.
+// lanes by DPP and swaps), or by the 256 threads of a workgroup when it is
+// wider than a wave holds.  All sums and statistics are fp32.  Measured: 2048^2
+// cells of 64 channels in bf16 forward 182 us (5.9 TB/s), backward 322 us (5.0);
+// 1024 x 1792 of 256, fp32 in and bf16 out, 460 us (6.1) and 907 us (5.2), where
+// a large copy moves 4.8.
 //
 // dgamma and dbeta: every thread keeps the sums of its own columns over the
 // cells it visits, a workgroup adds its threads in a fixed order and writes one

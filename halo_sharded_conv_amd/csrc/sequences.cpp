@@ -14,7 +14,7 @@ namespace st {
 // Four-wave tiles serve long sequences; a sequence with at most two waves'
 // worth of rows (keys) goes to one-wave workgroups, so a single token or a small
 // window does not leave three waves idle.
-AttnShape attn_shape(st_dtype dtype, int dp) {
+AttnShape attn_shape(st_dtype dtype) {
   AttnShape s{};
   const bool f32 = dtype == ST_F32;
   s.tile[kListForward][0] = 128;
@@ -188,7 +188,7 @@ st_status st_plan_sequences(int32_t nseq, const int32_t* q_lens, const int32_t* 
     p->dtype = dtype;
     p->total_q = tq;
     p->total_k = tk;
-    p->shape = attn_shape(dtype, p->dp);
+    p->shape = attn_shape(dtype);
     try {
       for (int l = 0; l < kLists; ++l) build(p, seqs, l);
     } catch (...) {

@@ -42,7 +42,7 @@ struct AttnShape {
   int fill[kLists][2];      // workgroups that fill the GPU
 };
 inline int attn_padded_dim(int dim) { return dim <= 32 ? 32 : dim <= 64 ? 64 : dim <= 96 ? 96 : 128; }
-AttnShape attn_shape(st_dtype dtype, int padded_dim);
+AttnShape attn_shape(st_dtype dtype);
 
 }  // namespace st
 
