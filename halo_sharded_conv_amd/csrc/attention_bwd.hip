@@ -137,10 +137,11 @@ __global__ __launch_bounds__(64 * NW, (dq_waves<T, DP>())) void attn_dq(const At
         if (b == 0 && j0 == 0) {
           // A row with all its keys in these 32 takes D as the sum of p dp in
           // fp32: `out` is rounded to its type, and with few keys that rounding
-          // is as large as all others together.
-          float d = 0.f;
+          // is as large as all others together.  A single key weighs exactly one,
+          // so that nothing is left of dq and dk.
+          float d = (limit == 1 ? 1.f : s[0]) * dp[0];
 #pragma unroll
-          for (int r = 0; r < 16; ++r) d = fmaf(s[r], dp[r], d);
+          for (int r = 1; r < 16; ++r) d = fmaf(s[r], dp[r], d);
           d = half_sum(d);
           delta = limit <= 32 ? d : delta;
         }

@@ -171,6 +171,20 @@ def test_large_scores(gpu_lib):
         check(r, *host, [n], [n], dtype, False, 0.5)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("q_lens,k_lens,heads,kv_heads,dim", [
+    ([0, 1, 0, 1, 1], None, 8, 1, 128),
+    ([1, 200, 33], [1, 1, 1], 4, 2, 64),
+    ([300], [1], 3, 3, 96)])
+def test_a_single_key_leaves_no_gradient_of_its_weight(gpu_lib, q_lens, k_lens, heads, kv_heads, dim, dtype):
+    # its weight is one whatever q and k are: exact zeros, not the roundings of p dp - D
+    k_lens = k_lens or q_lens
+    t = [x.cuda() for x in inputs(q_lens, k_lens, heads, kv_heads, dim, dtype, seed=12)]
+    r = run(gpu_lib, *t, q_lens, k_lens, dtype, False, dim ** -0.5)
+    check(r, *t, q_lens, k_lens, dtype, False, dim ** -0.5)
+    assert not r["dq"].any() and not r["dk"].any()
+
+
 @pytest.mark.parametrize("layout", ["joint", "heads first", "spaced"])
 def test_strides(gpu_lib, layout):
     """Views: a joint projection, heads outermost, rows with gaps; values
