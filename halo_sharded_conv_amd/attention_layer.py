@@ -23,7 +23,7 @@ from typing import Optional, Sequence
 
 import numpy as np
 
-from . import (ST_BF16, ST_F32, ShardConvError, _cells, st_attention_packed, st_attention_packed_backward,
+from . import (ST_BF16, ST_F32, ShardConvError, _cells, _stream, st_attention_packed, st_attention_packed_backward,
                st_attention_workspace_bytes, st_conv_dgrad_weights, st_conv_sharded, st_conv_wgrad,
                st_conv_wgrad_workspace_bytes, st_conv_workspace_bytes, st_layernorm_backward,
                st_layernorm_backward_workspace_bytes, st_layernorm_sharded, st_plan_positions, st_plan_sequences,
@@ -84,6 +84,7 @@ class ShardedAttention:
         self.positions = torch.zeros(t, nd, dtype=torch.int32, device=self.device)
         st_plan_positions(self.x_plan, self.parts(self.positions))
         self.gamma = self.beta = None
+        self._gamma, self._beta = (torch.ones(channels, device=self.device) for _ in range(2))
         self.w_qkv = torch.zeros(joint * channels, dtype=bf16, device=self.device)
         self.w_out = torch.zeros(channels * width, dtype=bf16, device=self.device)
         ws = [st_conv_workspace_bytes(self.norm_plan, joint, 1), st_conv_workspace_bytes(self.width_plan, channels, 1)]
@@ -93,6 +94,7 @@ class ShardedAttention:
         self.attn_ws = torch.zeros(max(16, st_attention_workspace_bytes(self.seqs, True)), dtype=torch.uint8,
                                    device=self.device)
         self.grads = None
+        torch.cuda.synchronize()             # the steps may run on any stream: nothing is left to fill
 
     def parts(self, packed) -> list:
         """The shards' views of a packed [tokens, ...] buffer."""
@@ -106,12 +108,16 @@ class ShardedAttention:
 
     def set_weights(self, w_qkv: np.ndarray, w_out: np.ndarray, gamma=None, beta=None) -> None:
         """w_qkv [(heads + 2 kv_heads) * head_dim, channels], w_out [channels,
-        heads * head_dim] as float32 (rounded to bf16); gamma, beta [channels]."""
+        heads * head_dim] as float32 (rounded to bf16); gamma, beta [channels].
+        Waits for the device before and after: steps on any stream see one set
+        of weights."""
         torch = _torch()
+        torch.cuda.synchronize()
         self.w_qkv.copy_(torch.from_numpy(np.ascontiguousarray(w_qkv, np.float32).reshape(-1)))
         self.w_out.copy_(torch.from_numpy(np.ascontiguousarray(w_out, np.float32).reshape(-1)))
-        put = lambda a: None if a is None else torch.from_numpy(np.ascontiguousarray(a, np.float32)).to(self.device)  # noqa: E731
-        self.gamma, self.beta = put(gamma), put(beta)
+        put = lambda a, to: None if a is None else to.copy_(torch.from_numpy(np.asarray(a, np.float32).reshape(to.shape)))  # noqa: E731
+        self.gamma, self.beta = put(gamma, self._gamma), put(beta, self._beta)
+        torch.cuda.synchronize()
 
     # ------------------------------------------------------------- steps
     def forward(self, x, stream=None):
@@ -133,7 +139,12 @@ class ShardedAttention:
                         workspace=self.conv_ws, stream=stream)
         return self.y
 
-    def _alloc_backward(self) -> dict:
+    def alloc_backward(self) -> None:
+        """The buffers of the backward steps.  The first backward() calls it; call
+        it before a graph capture whose steps run on another stream than the
+        current one."""
+        if self.grads is not None:
+            return
         torch = _torch()
         t, dev = self.tokens, self.device
         f32, bf16 = torch.float32, torch.bfloat16
@@ -144,25 +155,26 @@ class ShardedAttention:
                    st_conv_workspace_bytes(self.joint_plan, self.channels, 1))
         if conv == 0:
             raise ShardConvError(4, "unsupported channel counts")
-        g = {"wide": torch.zeros(t, self.width, dtype=f32, device=dev),
-             "dout": torch.zeros(t, self.width, dtype=bf16, device=dev),
-             "dqkv": torch.zeros(t, self.joint_width, dtype=bf16, device=dev),
-             "dnorm": torch.zeros(t, self.channels, dtype=f32, device=dev),
-             "dx": torch.zeros(t, self.channels, dtype=f32, device=dev),
-             "dw_qkv": torch.zeros(self.joint_width, self.channels, dtype=f32, device=dev),
-             "dw_out": torch.zeros(self.channels, self.width, dtype=f32, device=dev),
-             "dgamma": torch.zeros(self.channels, dtype=f32, device=dev),
-             "dbeta": torch.zeros(self.channels, dtype=f32, device=dev),
-             "wt": torch.zeros(max(self.w_qkv.numel(), self.w_out.numel()), dtype=bf16, device=dev),
-             "ws": torch.zeros(need, dtype=torch.uint8, device=dev),
-             "conv_ws": torch.zeros(conv, dtype=torch.uint8, device=dev)}
-        return g
+        new = lambda *shape, dt=f32: torch.empty(*shape, dtype=dt, device=dev)  # noqa: E731
+        g = {"wide": new(t, self.width), "dout": new(t, self.width, dt=bf16), "dqkv": new(t, self.joint_width, dt=bf16),
+             "dnorm": new(t, self.channels), "dx": new(t, self.channels),
+             "dw_qkv": new(self.joint_width, self.channels), "dw_out": new(self.channels, self.width),
+             "dgamma": new(self.channels), "dbeta": new(self.channels),
+             "wt": new(max(self.w_qkv.numel(), self.w_out.numel()), dt=bf16),
+             "ws": new(need, dt=torch.uint8), "conv_ws": new(conv, dt=torch.uint8)}
+        # Nothing is filled, but the memory may have had another owner, whose work
+        # the current stream alone has in order: the steps may run on another.
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.synchronize()
+        self.grads = g
 
     def backward(self, x, dy, stream=None) -> dict:
         """Gradients of the last forward(x) for dy (packed bf16 [tokens,
         channels]): dx (fp32, packed), dw_qkv, dw_out, dgamma, dbeta."""
         if self.grads is None:
-            self.grads = self._alloc_backward()
+            if _stream(stream).value != _stream(None).value and _torch().cuda.is_current_stream_capturing():
+                raise ShardConvError(4, "the backward buffers are not there yet: call alloc_backward() before capturing")
+            self.alloc_backward()
         g, parts, nd = self.grads, self.parts, self.nd
         # the output projection: weight gradient, then the gradient at the
         # attention's output, rounded to bf16

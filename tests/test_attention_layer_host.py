@@ -1,0 +1,72 @@
+"""The attention branch's own bookkeeping without a GPU: the library's launching
+calls are replaced by recorders, the plans are the library's."""
+import numpy as np
+import pytest
+import torch
+
+import halo_sharded_conv_amd as hsc
+from halo_sharded_conv_amd import attention_layer
+
+LAUNCHES = ("st_layernorm_sharded", "st_conv_sharded", "st_rope_axes", "st_attention_packed", "st_conv_wgrad",
+            "st_conv_dgrad_weights", "st_attention_packed_backward", "st_layernorm_backward", "st_plan_positions")
+
+
+@pytest.fixture
+def events(monkeypatch):
+    """Names of the launches and "synchronize", in order, with their arguments."""
+    log = []
+    for n in LAUNCHES:
+        monkeypatch.setattr(attention_layer, n, lambda *a, _n=n, **kw: log.append((_n, a, kw)))
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda *a: log.append(("synchronize", a, {})))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(attention_layer, "_stream", lambda s: hsc.ctypes.c_void_p(s or 0), raising=False)
+    return log
+
+
+def names(log):
+    return [e[0] for e in log]
+
+
+def make(spatial=(4, 6), shards=((2, 2), (6,)), channels=32, heads=2, kv_heads=1, head_dim=16):
+    return attention_layer.ShardedAttention(spatial, shards, channels, heads, kv_heads, head_dim, device="cpu")
+
+
+def test_buffers_are_ready_for_any_stream(events):
+    """Steps may run on a stream that is not the current one: everything the
+    constructor and set_weights queue is waited for."""
+    layer = make()
+    assert names(events)[-1] == "synchronize"
+    events.clear()
+    layer.set_weights(np.ones((64, 32)), np.ones((32, 32)), np.ones(32), np.zeros(32))
+    assert names(events) == ["synchronize", "synchronize"]     # older steps have read, later ones see
+
+
+def test_weights_stay_in_place(events):
+    """A captured graph keeps their addresses, and no step reads a freed buffer."""
+    layer = make()
+    layer.set_weights(np.ones((64, 32)), np.ones((32, 32)), np.ones(32), np.zeros(32))
+    at = [t.data_ptr() for t in (layer.w_qkv, layer.w_out, layer.gamma, layer.beta)]
+    layer.set_weights(np.ones((64, 32)), np.ones((32, 32)), 2 * np.ones(32), np.ones(32))
+    assert at == [t.data_ptr() for t in (layer.w_qkv, layer.w_out, layer.gamma, layer.beta)]
+    assert float(layer.gamma[0]) == 2 and float(layer.beta[0]) == 1
+
+
+def test_first_backward_on_a_stream_of_its_own(events, monkeypatch):
+    layer = make()
+    x, dy = torch.zeros(24, 32), torch.zeros(24, 32, dtype=torch.bfloat16)
+    events.clear()
+    layer.backward(x, dy, stream=7)
+    assert names(events)[0] == "synchronize" and names(events).count("synchronize") == 1
+    events.clear()
+    grads = layer.grads
+    layer.backward(x, dy, stream=7)
+    assert "synchronize" not in names(events) and layer.grads is grads
+    # inside a capture nothing can be waited for
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    other = make()
+    with pytest.raises(hsc.ShardConvError):
+        other.backward(x, dy, stream=7)
+    events.clear()
+    other.backward(x, dy)
+    assert "synchronize" not in names(events)

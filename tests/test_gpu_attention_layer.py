@@ -94,3 +94,32 @@ def test_refusals(gpu_lib):
         ShardedAttention((6, 10), ((3, 3), (10,)), 32, 4, 2, 16, batch=2)
     with pytest.raises(gpu_lib.ShardConvError):
         ShardedAttention((6, 10), ((6,), (10,)), 32, 4, 3, 16)
+
+
+def test_steps_on_a_stream_of_their_own(gpu_lib):
+    """Constructor, weights and the first backward while the current stream is
+    busy, every step on another stream: the bits of a run on one stream."""
+    from halo_sharded_conv_amd.attention_layer import ShardedAttention
+    rng = np.random.default_rng(2)
+    w_qkv, w_out = rng.normal(size=(4 * 16 + 2 * 2 * 16, 32)) / 6, rng.normal(size=(32, 64)) / 8
+    gamma, beta = 1 + 0.2 * rng.normal(size=32), 0.2 * rng.normal(size=32)
+    x = torch.from_numpy(np.float32(rng.normal(size=(60, 32)))).cuda()
+    dy = torch.from_numpy(rng.normal(size=(60, 32))).bfloat16().cuda()
+    busy = torch.empty(1 << 29, device="cuda")
+    torch.cuda.synchronize()
+
+    def steps(stream):
+        for _ in range(20):
+            busy.fill_(1.0)
+        layer = ShardedAttention((6, 10), ((2, 4), (10,)), 32, 4, 2, 16)
+        layer.set_weights(w_qkv, w_out, gamma, beta)
+        layer.forward(x, stream)
+        for _ in range(20):
+            busy.fill_(2.0)
+        r = layer.backward(x, dy, stream)
+        torch.cuda.synchronize()
+        return {"y": layer.y, **r}
+
+    want, got = steps(None), steps(torch.cuda.Stream())
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
