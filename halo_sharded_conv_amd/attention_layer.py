@@ -70,6 +70,11 @@ class ShardedAttention:
         cells = _cells(self.x_plan)
         self.starts = [sum(cells[:i]) for i in range(len(cells) + 1)]
         self.tokens = t = self.starts[-1]
+        # every other packed buffer is cut into shard buffers; the narrowest rows
+        # are the bf16 ones of the volume (normed, dy)
+        if any(s * channels * 2 % 16 for s in self.starts[:-1]):
+            raise ShardConvError(7, f"the packed shards of {channels} channels do not start on 16 bytes: "
+                                    "use a multiple of 8 channels")
         self.device = torch.device(device)
         lens = [t // batch] * batch
         self.seqs = st_plan_sequences(lens, None, heads, kv_heads, head_dim, ST_BF16, causal=False)
@@ -81,8 +86,11 @@ class ShardedAttention:
         self.attended, self.y = new(width, bf16), new(channels, f32)
         self.stats = torch.zeros(t, 2, device=self.device)
         self.lse = torch.zeros(t, heads, device=self.device)
-        self.positions = torch.zeros(t, nd, dtype=torch.int32, device=self.device)
-        st_plan_positions(self.x_plan, self.parts(self.positions))
+        # (written shard by shard, then packed: a shard of the packed rows starts
+        # wherever the cells before it end, a buffer of its own on 16 bytes)
+        own = [torch.empty(n, nd, dtype=torch.int32, device=self.device) for n in cells]
+        st_plan_positions(self.x_plan, own)
+        self.positions = torch.cat(own)
         self.gamma = self.beta = None
         self._gamma, self._beta = (torch.ones(channels, device=self.device) for _ in range(2))
         self.w_qkv = torch.zeros(joint * channels, dtype=bf16, device=self.device)

@@ -70,3 +70,25 @@ def test_first_backward_on_a_stream_of_its_own(events, monkeypatch):
     events.clear()
     other.backward(x, dy)
     assert "synchronize" not in names(events)
+
+
+@pytest.mark.parametrize("spatial,shards", [((9, 15), ((5, 4), (15,))), ((9, 7), ((5, 4), (4, 3))),
+                                            ((5, 7, 9), ((2, 3), (7,), (9,)))])
+def test_odd_shards_have_aligned_buffers(events, spatial, shards):
+    layer = make(spatial, shards, channels=40)
+    launch = next(e for e in events if e[0] == "st_plan_positions")
+    assert all(t.data_ptr() % 16 == 0 for t in launch[1][1])
+    events.clear()
+    t = layer.tokens
+    layer.forward(torch.zeros(t, 40))
+    layer.backward(torch.zeros(t, 40), torch.zeros(t, 40, dtype=torch.bfloat16))
+    lists = [b for e in events for b in e[1] if isinstance(b, list) and torch.is_tensor(b[0])]
+    assert len(lists) > 10 and all(b.data_ptr() % 16 == 0 for shard in lists for b in shard)
+
+
+def test_widths_whose_packed_shards_are_not_aligned(events):
+    with pytest.raises(hsc.ShardConvError) as e:
+        make((9, 15), ((5, 4), (15,)), channels=36)
+    assert e.value.status == 7
+    make((9, 16), ((5, 4), (16,)), channels=36)            # the shards of this cut do
+    make((9, 15), ((9,), (15,)), channels=36)              # and so does a single one

@@ -123,3 +123,26 @@ def test_steps_on_a_stream_of_their_own(gpu_lib):
     want, got = steps(None), steps(torch.cuda.Stream())
     for n in want:
         assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("spatial,shards", [((9, 7), ((5, 4), (4, 3))), ((5, 7, 9), ((2, 3), (7,), (4, 5)))])
+def test_odd_shards(gpu_lib, spatial, shards):
+    """Shards that start after an odd number of cells."""
+    from halo_sharded_conv_amd.attention_layer import ShardedAttention
+    rng = np.random.default_rng(3)
+    c = 40
+    layer = ShardedAttention(spatial, shards, c, 3, 1, 16)
+    t = layer.tokens
+    pos = layer.positions.cpu().numpy()
+    assert sorted(map(tuple, pos)) == sorted(np.ndindex(*spatial))
+    x = np.float32(rng.normal(size=(t, c)) + 0.3)
+    w_qkv = bf16(rng.normal(size=(layer.joint_width, c)) / np.sqrt(c))
+    w_out = bf16(rng.normal(size=(c, layer.width)) / np.sqrt(layer.width))
+    gamma, beta = np.float32(1 + 0.2 * rng.normal(size=c)), np.float32(0.2 * rng.normal(size=c))
+    dy = bf16(rng.normal(size=(t, c)))
+    layer.set_weights(w_qkv, w_out, gamma, beta)
+    xd, dyd = torch.from_numpy(x).cuda(), torch.from_numpy(dy).bfloat16().cuda()
+    got = {"y": layer.forward(xd), **layer.backward(xd, dyd)}
+    want = reference(layer, x.astype(np.float64), pos, w_qkv, w_out, gamma, beta, dy, [t])
+    errs = {n: off(got[n].double().cpu().numpy().reshape(want[n].shape), want[n]) for n in want}
+    assert all(e < 0.02 for e in errs.values()), errs
