@@ -626,6 +626,36 @@ __all__ = [
 
 # ------------------------------------------------------------ token operators
 
+def _bits(*names):
+    return frozenset(getattr(_torch(), n) for n in names)
+
+
+# What the token operators take as fp32, bf16 and int32: the type itself, or its
+# bits (integers of its width, bytes).  Any other type is refused, not read as bits.
+_FP32, _INT32 = _bits("float32", "int32", "uint8"), _bits("int32", "uint8")
+_TYPES = {ST_F32: _FP32, ST_BF16: _bits("bfloat16", "int16", "uint8")}
+
+
+def _typed(t, what: str, types, min_bytes: int = 0) -> int:
+    """_dev_ptr of a tensor of one of these types, or of None."""
+    if t is not None and getattr(t, "is_cuda", False) and t.dtype not in types:
+        raise ShardConvError(1, f"{what}: unexpected dtype {t.dtype}")
+    return _dev_ptr(t, what, min_bytes)
+
+
+def _typed_array(tensors, what: str, types, sizes: List[int]):
+    arr = _ptr_array(tensors, what, sizes)
+    for i, t in enumerate(tensors):
+        if t is not None and t.dtype not in types:
+            raise ShardConvError(1, f"{what}[{i}]: unexpected dtype {t.dtype}")
+    return arr
+
+
+def _plan_array(plan: Plan, tensors, what: str):
+    """Shard buffers of a plan, in its dtype."""
+    return _typed_array(tensors, what, _TYPES[plan.dtype], _shard_bytes(plan))
+
+
 def _cells(plan: Plan) -> List[int]:
     """Interior cells of every shard."""
     if plan._cells is None:
@@ -643,11 +673,11 @@ def st_layernorm_sharded(x_plan: Plan, x_bufs, gamma, beta, eps: float, y_plan: 
                          stream=None) -> None:
     """Layer norm over the channels of every cell; stats: 2 floats per cell
     (mean, 1 / sqrt(var + eps)), shard by shard, or None."""
-    xs = _ptr_array(x_bufs, "st_layernorm_sharded x", _shard_bytes(x_plan))
-    ys = _ptr_array(y_bufs, "st_layernorm_sharded y", _shard_bytes(y_plan))
-    g = _dev_ptr(gamma, "gamma", 4 * x_plan.channels)
-    b = _dev_ptr(beta, "beta", 4 * x_plan.channels)
-    st = _dev_ptr(stats, "stats", 8 * sum(_cells(x_plan)))
+    xs = _plan_array(x_plan, x_bufs, "st_layernorm_sharded x")
+    ys = _plan_array(y_plan, y_bufs, "st_layernorm_sharded y")
+    g = _typed(gamma, "gamma", _FP32, 4 * x_plan.channels)
+    b = _typed(beta, "beta", _FP32, 4 * x_plan.channels)
+    st = _typed(stats, "stats", _FP32, 8 * sum(_cells(x_plan)))
     _check(lib.st_layernorm_sharded(x_plan.handle, xs, g, b, float(eps), y_plan.handle, ys, st, _stream(stream)),
            "st_layernorm_sharded")
 
@@ -659,20 +689,20 @@ def st_layernorm_backward_workspace_bytes(x_plan: Plan) -> int:
 def st_layernorm_backward(x_plan: Plan, x_bufs, dy_plan: Plan, dy_bufs, gamma, stats, dx_plan: Plan, dx_bufs, dgamma,
                           dbeta, workspace, stream=None) -> None:
     """stats: as st_layernorm_sharded wrote them; dgamma, dbeta: C floats or None."""
-    xs = _ptr_array(x_bufs, "st_layernorm_backward x", _shard_bytes(x_plan))
-    dys = _ptr_array(dy_bufs, "st_layernorm_backward dy", _shard_bytes(dy_plan))
-    dxs = _ptr_array(dx_bufs, "st_layernorm_backward dx", _shard_bytes(dx_plan))
+    xs = _plan_array(x_plan, x_bufs, "st_layernorm_backward x")
+    dys = _plan_array(dy_plan, dy_bufs, "st_layernorm_backward dy")
+    dxs = _plan_array(dx_plan, dx_bufs, "st_layernorm_backward dx")
     c = 4 * x_plan.channels
     ws, nb = _ws(workspace)
-    _check(lib.st_layernorm_backward(x_plan.handle, xs, dy_plan.handle, dys, _dev_ptr(gamma, "gamma", c),
-                                     _dev_ptr(stats, "stats", 8 * sum(_cells(x_plan))), dx_plan.handle, dxs,
-                                     _dev_ptr(dgamma, "dgamma", c), _dev_ptr(dbeta, "dbeta", c), ws, nb,
+    _check(lib.st_layernorm_backward(x_plan.handle, xs, dy_plan.handle, dys, _typed(gamma, "gamma", _FP32, c),
+                                     _typed(stats, "stats", _FP32, 8 * sum(_cells(x_plan))), dx_plan.handle, dxs,
+                                     _typed(dgamma, "dgamma", _FP32, c), _typed(dbeta, "dbeta", _FP32, c), ws, nb,
                                      _stream(stream)), "st_layernorm_backward")
 
 
 def st_plan_positions(plan: Plan, pos_bufs, stream=None) -> None:
     """Global int32 grid positions [N][extent...][ndim] of every shard's cells."""
-    ps = _ptr_array(pos_bufs, "st_plan_positions", [4 * plan.ndim * n for n in _cells(plan)])
+    ps = _typed_array(pos_bufs, "st_plan_positions", _INT32, [4 * plan.ndim * n for n in _cells(plan)])
     _check(lib.st_plan_positions(plan.handle, ps, _stream(stream)), "st_plan_positions")
 
 
@@ -800,7 +830,7 @@ def st_attention_packed(seqs: Sequences, q, k, v, scale: float, out, lse=None, w
     head_dim]; any strides that are multiples of 16 bytes; lse: float32
     [total queries, heads] or None."""
     what = "st_attention_packed"
-    l = _dev_ptr(lse, "st_attention_packed lse", 4 * seqs.total_q * seqs.heads)
+    l = _typed(lse, "st_attention_packed lse", _FP32, 4 * seqs.total_q * seqs.heads)
     ws, nb = _ws(workspace)
     _check(lib.st_attention_packed(seqs.handle, _tokens(q, "st_attention_packed q", seqs, False),
                                    _tokens(k, "st_attention_packed k", seqs, True),
@@ -815,7 +845,7 @@ def st_attention_packed_backward(seqs: Sequences, q, k, v, out, lse, dout, scale
         return _tokens(t, n, seqs, keys)
 
     what = "st_attention_packed_backward"
-    l = _dev_ptr(lse, "st_attention_packed_backward lse", 4 * seqs.total_q * seqs.heads)
+    l = _typed(lse, "st_attention_packed_backward lse", _FP32, 4 * seqs.total_q * seqs.heads)
     ws, nb = _ws(workspace)
     _check(lib.st_attention_packed_backward(
         seqs.handle, view(q, "st_attention_packed_backward q", False), view(k, "st_attention_packed_backward k", True),

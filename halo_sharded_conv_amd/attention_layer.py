@@ -23,9 +23,9 @@ from typing import Optional, Sequence
 
 import numpy as np
 
-from . import (ST_BF16, ST_F32, ShardConvError, _cells, _stream, st_attention_packed, st_attention_packed_backward,
-               st_attention_workspace_bytes, st_conv_dgrad_weights, st_conv_sharded, st_conv_wgrad,
-               st_conv_wgrad_workspace_bytes, st_conv_workspace_bytes, st_layernorm_backward,
+from . import (_TYPES, ST_BF16, ST_F32, ShardConvError, _cells, _stream, st_attention_packed,
+               st_attention_packed_backward, st_attention_workspace_bytes, st_conv_dgrad_weights, st_conv_sharded,
+               st_conv_wgrad, st_conv_wgrad_workspace_bytes, st_conv_workspace_bytes, st_layernorm_backward,
                st_layernorm_backward_workspace_bytes, st_layernorm_sharded, st_plan_positions, st_plan_sequences,
                st_plan_shards, st_rope_axes)
 
@@ -183,6 +183,8 @@ class ShardedAttention:
             if _stream(stream).value != _stream(None).value and _torch().cuda.is_current_stream_capturing():
                 raise ShardConvError(4, "the backward buffers are not there yet: call alloc_backward() before capturing")
             self.alloc_backward()
+        if dy.dtype not in _TYPES[ST_BF16]:
+            raise ShardConvError(1, f"dy: expected bfloat16, got {dy.dtype}")
         g, parts, nd = self.grads, self.parts, self.nd
         # the output projection: weight gradient, then the gradient at the
         # attention's output, rounded to bf16

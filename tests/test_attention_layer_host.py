@@ -92,3 +92,14 @@ def test_widths_whose_packed_shards_are_not_aligned(events):
     assert e.value.status == 7
     make((9, 16), ((5, 4), (16,)), channels=36)            # the shards of this cut do
     make((9, 15), ((9,), (15,)), channels=36)              # and so does a single one
+
+
+def test_upstream_gradient_of_another_type(events):
+    """An fp32 dy is refused, not read as bf16 bits."""
+    layer = make()
+    x = torch.zeros(24, 32)
+    events.clear()
+    with pytest.raises(hsc.ShardConvError) as e:
+        layer.backward(x, torch.zeros(24, 32))
+    assert e.value.status == 1 and not [n for n in names(events) if n != "synchronize"]
+    layer.backward(x, torch.zeros(24, 32, dtype=torch.int16))  # bf16 bits

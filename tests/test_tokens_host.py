@@ -148,3 +148,53 @@ def test_positions_refusals():
     assert lib.st_plan_positions(None, None, None) == INVALID
     assert lib.st_plan_positions(a.handle, (ctypes.c_void_p * 1)(0), None) == INVALID
     assert lib.st_plan_positions(a.handle, (ctypes.c_void_p * 1)(20), None) == ALIGN
+
+
+class Device:
+    """A tensor of some type on the GPU, at an address that no call accepts."""
+    is_cuda = True
+
+    def __init__(self, dtype, n=1 << 20):
+        self.dtype, self.nbytes = dtype, n
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 4
+
+
+def test_types_that_are_not_read_as_bits():
+    """Every buffer of the layer norm, the positions and lse has its type or is
+    raw bits; the right types get as far as the address."""
+    f32, bf16 = hsc.st_plan_shards(2, 1, 8, (4, 4), ((4,), (4,)), (0, 0), "f32"), hsc.st_plan_shards(
+        2, 1, 8, (4, 4), ((4,), (4,)), (0, 0), "bf16")
+    t = hsc._torch()
+    x, y, s = Device(t.float32), Device(t.bfloat16), Device(t.float32)
+
+    def status(f):
+        with pytest.raises(hsc.ShardConvError) as e:
+            f()
+        return e.value.status
+
+    def forward(x=x, y=y, g=s, b=s, st=s):
+        return status(lambda: hsc.st_layernorm_sharded(f32, [x], g, b, 1e-5, bf16, [y], st, stream=0))
+
+    def backward(x=x, dy=y, g=s, st=s, dx=x, dg=s, db=s):
+        return status(lambda: hsc.st_layernorm_backward(f32, [x], bf16, [dy], g, st, f32, [dx], dg, db, s, stream=0))
+
+    assert forward() == ALIGN and backward() == ALIGN
+    assert forward(x=Device(t.int32), y=Device(t.int16), st=Device(t.uint8)) == ALIGN
+    for wrong in (t.float64, t.float16, t.bfloat16, t.int64):
+        w = Device(wrong)
+        assert [forward(x=w), forward(g=w), forward(b=w), forward(st=w)] == [INVALID] * 4, wrong
+        assert [backward(x=w), backward(g=w), backward(st=w), backward(dx=w), backward(dg=w), backward(db=w)] == [INVALID] * 6
+    for wrong in (t.float32, t.float16, t.int32):
+        assert forward(y=Device(wrong)) == INVALID and backward(dy=Device(wrong)) == INVALID, wrong
+    assert status(lambda: hsc.st_plan_positions(f32, [Device(t.int32)], stream=0)) == ALIGN
+    for wrong in (t.int64, t.int16, t.float32):
+        assert status(lambda: hsc.st_plan_positions(f32, [Device(wrong)], stream=0)) == INVALID
+    one = seqs([8])
+    for wrong in (t.float64, t.bfloat16, t.int64):
+        assert status(lambda: hsc.st_attention_packed(one, None, None, None, 0.1, None, Device(wrong), stream=0)) == INVALID
+        assert status(lambda: hsc.st_attention_packed_backward(one, *[None] * 4, Device(wrong), None, 0.1, *[None] * 4, stream=0)) == INVALID
