@@ -20,6 +20,8 @@ st_status hip_check(hipError_t e, const char* what);
 // Reports the launch status of the kernels just enqueued.
 st_status launch_check(const char* what);
 bool aligned16(const void* p);
+// Workgroups of a launch: HIP takes fewer than 2^32 threads along an axis.
+constexpr int64_t max_blocks(int threads) { return 0xFFFFFFFFll / threads; }
 
 // Geometry is held with three spatial axes; a 2D plan has a leading axis of
 // extent 1, halo 0 and one shard.

@@ -51,6 +51,7 @@ struct LnShard {
 struct LnArgs {
   int32_t nshards, channels, lpr_log2, flat;   // flat: bit i set where tensor i has no margins
   int32_t blocks, parts;
+  int32_t block0;                     // forward: this launch's first block
   int32_t out_bf16;
   float eps, count;
   const float* gamma;
@@ -118,8 +119,9 @@ __global__ __launch_bounds__(kLnThreads) void ln_forward(const LnArgs a) {
   const int lpr = BLOCK ? kLnThreads : 1 << a.lpr_log2;
   const int sub = threadIdx.x & (lpr - 1), slot = threadIdx.x / lpr, rp = kLnThreads / lpr;
   const int C = a.channels;
-  const LnShard& s = a.sh[shard_of(a, blockIdx.x)];
-  const int r0 = ((int)blockIdx.x - s.block_begin) * (rp * U) + slot;
+  const int blk = a.block0 + (int)blockIdx.x;
+  const LnShard& s = a.sh[shard_of(a, blk)];
+  const int r0 = (blk - s.block_begin) * (rp * U) + slot;
   float x[U][NV][VEC], sum[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -415,14 +417,15 @@ st_status ln_geometry(LnArgs& a, const st_plan* p, const LnPick& pick, bool back
     v.row_begin = rows;
     rows += n;
     blocks += (n + rpb - 1) / rpb;
-    if (blocks >= (1ll << 31)) return fail(ST_ERR_UNSUPPORTED, "layer norm: too many cells");
+    // (the backward pass steps by up to kLnMaxParts past the last block)
+    if (blocks >= (1ll << 31) - kLnMaxParts) return fail(ST_ERR_UNSUPPORTED, "layer norm: too many cells");
   }
   a.blocks = (int32_t)blocks;
   return ST_OK;
 }
 
-template <class TX> st_status ln_forward_launch(const LnArgs& a, const LnPick& p, hipStream_t st) {
-  const dim3 grid(a.blocks), block(kLnThreads);
+template <class TX> st_status ln_forward_launch(const LnArgs& a, const LnPick& p, int blocks, hipStream_t st) {
+  const dim3 grid(blocks), block(kLnThreads);
 #define LN_CASE(V, N, B) \
   if (p.vec == V && p.nv == N && p.block == B) { ln_forward<TX, V, N, B><<<grid, block, 0, st>>>(a); return launch_check("ln_forward"); }
   if constexpr (TX::kSize == 2) {                       // (8 a lane: both sides bf16)
@@ -485,7 +488,13 @@ st_status st_layernorm_sharded(const st_plan* x_plan, const void* const* x_bufs,
   a.stats = stats_or_null;
   a.out_bf16 = y_plan->dtype == ST_BF16;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  return x_plan->dtype == ST_BF16 ? ln_forward_launch<BF16>(a, pick, st) : ln_forward_launch<F32>(a, pick, st);
+  for (int64_t b = 0; b < a.blocks; b += max_blocks(kLnThreads)) {
+    a.block0 = (int32_t)b;
+    const int n = (int)std::min<int64_t>(a.blocks - b, max_blocks(kLnThreads));
+    s = x_plan->dtype == ST_BF16 ? ln_forward_launch<BF16>(a, pick, n, st) : ln_forward_launch<F32>(a, pick, n, st);
+    if (s != ST_OK) return s;
+  }
+  return ST_OK;
 }
 
 size_t st_layernorm_backward_workspace_bytes(const st_plan* x_plan) {

@@ -261,3 +261,22 @@ def test_refusals_on_the_gpu(gpu_lib):
     assert status(lambda: gpu_lib.st_layernorm_backward(s.plan, s.bufs, s.plan, s.bufs, None, stats, s.plan, s.bufs, None, None, None)) == 5
     g = torch.zeros(65, device="cuda")[1:]
     assert status(lambda: ln(s.plan, s.bufs, g, None, 1e-5, s.plan, s.bufs)) == 7
+
+
+def test_more_cells_than_one_launch_holds(gpu_lib):
+    """2^28 cells of 33 channels are 2^24 workgroups of 256 threads, one more than
+    a launch takes: the cells around the cut and the last ones are those of a
+    small call.  The backward pass has a fixed number of workgroups."""
+    n, c = (1 << 28) + 37, 33
+    x = torch.empty(n, c, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    g = torch.randn(c, device="cuda")
+    ends = [slice(0, 20), slice((1 << 28) - 40, (1 << 28) + 17), slice(n - 21, n)]
+
+    def forward(rows):
+        plan = gpu_lib.st_plan_shards(2, 1, c, (1, len(rows)), ((1,), (len(rows),)), (0, 0), "bf16")
+        gpu_lib.st_layernorm_sharded(plan, [rows], g, None, 1e-5, plan, [rows])
+        return rows
+
+    want = [forward(x[e].clone()) for e in ends]
+    forward(x)
+    assert all(torch.equal(x[e], w) for e, w in zip(ends, want))
