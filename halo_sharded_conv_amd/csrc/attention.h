@@ -20,6 +20,8 @@
 // once (no conflict counted in any kernel here).
 #pragma once
 
+#include <algorithm>
+
 #include "sequences.h"
 #include "tokens.h"
 
@@ -188,6 +190,17 @@ template <class T> __device__ __forceinline__ void store_block(char* row, const 
 }
 
 // ---- host side
+
+// Work items of one launch, a workgroup per item and key-value head: list by
+// list, in as many launches as the items need.  launch(first item, workgroups)
+template <class F> st_status attn_launches(size_t items, int kv_heads, int threads, F launch) {
+  const size_t most = (size_t)(max_blocks(threads) / kv_heads);
+  for (size_t i = 0; i < items; i += most) {
+    const st_status r = launch(i, (int)(std::min(items - i, most) * kv_heads));
+    if (r != ST_OK) return r;
+  }
+  return ST_OK;
+}
 
 struct AttnLaunch {
   AttnArgs a;

@@ -346,15 +346,16 @@ template <class T, int DP> st_status forward_dim(st_seqs* s, AttnArgs a, hipStre
   for (int w = 0; w < 2; ++w) {
     if (l.item[w].empty()) continue;
     const int tile = l.tile[w];
-    a.items = l.d_item[w];
     a.joins = l.d_join[w];
     a.part = part;
     a.part2 = part + l.parts[w] * s->kv_heads * tile * (int64_t)DP;
     part = a.part2 + (l.parts[w] * s->kv_heads * tile + 63) / 64 * 64;
-    const int grid = (int)(l.item[w].size() * s->kv_heads);
-    if (w == 0) attn_forward<T, DP, KT, 4><<<grid, 256, 0, st>>>(a);
-    else attn_forward<T, DP, 32, 1><<<grid, 64, 0, st>>>(a);
-    st_status r = launch_check("attn_forward");
+    st_status r = attn_launches(l.item[w].size(), s->kv_heads, w == 0 ? 256 : 64, [&](size_t first, int grid) {
+      a.items = l.d_item[w] + first;
+      if (w == 0) attn_forward<T, DP, KT, 4><<<grid, 256, 0, st>>>(a);
+      else attn_forward<T, DP, 32, 1><<<grid, 64, 0, st>>>(a);
+      return launch_check("attn_forward");
+    });
     if (r != ST_OK) return r;
     if (l.join[w].empty()) continue;
     attn_join<T, DP><<<(int)(l.join[w].size() * s->kv_heads * tile), 256, 0, st>>>(a, tile);

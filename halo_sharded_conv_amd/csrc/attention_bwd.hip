@@ -521,18 +521,19 @@ template <class T, int DP> st_status backward_dim(st_seqs* s, AttnArgs a, hipStr
     for (int w = 0; w < 2; ++w) {                       // one list at a time: they share the partial buffer
       if (l.item[w].empty()) continue;
       const int tile = l.tile[w];
-      a.items = l.d_item[w];
       a.joins = l.d_join[w];
       a.part2 = a.part + l.parts[w] * s->kv_heads * tile * (int64_t)DP;
-      const int grid = (int)(l.item[w].size() * s->kv_heads);
-      if (rows) {
-        if (w == 0) attn_dq<T, DP, KT, 4><<<grid, 256, 0, st>>>(a);
-        else attn_dq<T, DP, 32, 1><<<grid, 64, 0, st>>>(a);
-      } else {
-        if (w == 0) attn_dkv<T, DP, KT, 4><<<grid, 256, 0, st>>>(a);
-        else attn_dkv<T, DP, 32, 1><<<grid, 64, 0, st>>>(a);
-      }
-      st_status r = launch_check(rows ? "attn_dq" : "attn_dkv");
+      st_status r = attn_launches(l.item[w].size(), s->kv_heads, w == 0 ? 256 : 64, [&](size_t first, int grid) {
+        a.items = l.d_item[w] + first;
+        if (rows) {
+          if (w == 0) attn_dq<T, DP, KT, 4><<<grid, 256, 0, st>>>(a);
+          else attn_dq<T, DP, 32, 1><<<grid, 64, 0, st>>>(a);
+        } else {
+          if (w == 0) attn_dkv<T, DP, KT, 4><<<grid, 256, 0, st>>>(a);
+          else attn_dkv<T, DP, 32, 1><<<grid, 64, 0, st>>>(a);
+        }
+        return launch_check(rows ? "attn_dq" : "attn_dkv");
+      });
       if (r != ST_OK) return r;
       if (l.join[w].empty()) continue;
       const int jg = (int)(l.join[w].size() * s->kv_heads * tile);

@@ -346,3 +346,16 @@ def test_refusals_on_the_gpu(gpu_lib):
     lse = torch.zeros(8, 2, device="cuda")
     assert status(lambda: b(seqs, t, t, t, t, lse, t, 0.1, t, t, t, None)) == 5
     assert status(lambda: b(seqs, t, t, t, t, None, t, 0.1, t, t, t, lse)) == 1
+
+
+def test_more_tiles_than_one_launch_holds(gpu_lib):
+    """2^22 sequences of one token with 16 heads are 2^26 one-wave workgroups, one
+    more than a launch takes.  A single key weighs one: out = v, dv = dout, and
+    nothing is left of dq and dk."""
+    n, heads, dim = (1 << 22) + 3, 16, 8
+    g = torch.Generator("cuda").manual_seed(1)
+    q, k, v, dout = (torch.empty(n, heads, dim, dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(4))
+    r = run(gpu_lib, q, k, v, dout, [1] * n, [1] * n, "bf16", False, 0.3)
+    assert torch.equal(r["out"], v) and torch.equal(r["dv"], dout)
+    assert not r["dq"].any() and not r["dk"].any()
+    assert bool(((r["lse"] - 0.3 * (q.float() * k.float()).sum(-1)).abs() < 1e-4).all())
