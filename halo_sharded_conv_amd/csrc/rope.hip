@@ -148,15 +148,17 @@ struct PosShard {
 };
 struct PosArgs {
   int32_t nshards, ndim;
+  int32_t block0;                         // this launch's first block
   PosShard sh[ST_MAX_SHARDS];
 };
 static_assert(sizeof(PosArgs) <= kMaxKernargBytes, "kernel argument struct too large");
 
 __global__ __launch_bounds__(256) void cell_positions(const PosArgs a) {
+  const int blk = a.block0 + (int)blockIdx.x;
   int i = 0;
-  while (i + 1 < a.nshards && a.sh[i + 1].block_begin <= (int)blockIdx.x) ++i;
+  while (i + 1 < a.nshards && a.sh[i + 1].block_begin <= blk) ++i;
   const PosShard& s = a.sh[i];
-  const int64_t r = (int64_t)((int)blockIdx.x - s.block_begin) * 256 + threadIdx.x;
+  const int64_t r = (int64_t)(blk - s.block_begin) * 256 + threadIdx.x;
   if (r >= s.rows) return;
   const uint32_t q = quo((uint32_t)r, s.w), w = (uint32_t)r - q * s.w.d;
   const uint32_t q2 = quo(q, s.h), h = q - q2 * s.h.d;
@@ -202,8 +204,14 @@ st_status st_plan_positions(const st_plan* plan, int32_t* const* pos_bufs, void*
     blocks += (rows + 255) / 256;
   }
   if (blocks >= (1ll << 31)) return err(ST_ERR_UNSUPPORTED, "too many cells");
-  cell_positions<<<(int)blocks, 256, 0, static_cast<hipStream_t>(stream)>>>(a);
-  return launch_check("cell_positions");
+  for (int64_t b = 0; b < blocks; b += max_blocks(256)) {
+    a.block0 = (int32_t)b;
+    const int n = (int)std::min<int64_t>(blocks - b, max_blocks(256));
+    cell_positions<<<n, 256, 0, static_cast<hipStream_t>(stream)>>>(a);
+    const st_status s = launch_check("cell_positions");
+    if (s != ST_OK) return s;
+  }
+  return ST_OK;
 }
 
 st_status st_rope_axes(const void* x, st_dtype x_dtype, int64_t x_token_stride, int64_t x_head_stride, int64_t tokens,

@@ -131,3 +131,15 @@ def test_refusals_on_the_gpu(gpu_lib):
     assert status(x, pos, [], x) == 4
     assert status(x, pos, [32, 32], x.double()) == 1
     assert status(x, pos, [32, 32], torch.zeros(1, 1, 64, device="cuda").expand(4, 2, 64)) == 2
+
+
+def test_positions_of_more_cells_than_one_launch_holds(gpu_lib):
+    """4.5e9 cells, over 2^32 threads: three samples in three shards of 5e8 columns."""
+    w = [500000001, 500000000, 499999999]
+    plan = gpu_lib.st_plan_shards(2, 3, 8, (1, sum(w)), ((1,), w), (0, 0), "bf16")
+    bufs = [torch.full((3, 1, n, 2), -1, dtype=torch.int32, device="cuda") for n in w]
+    gpu_lib.st_plan_positions(plan, bufs)
+    for i, b in enumerate(bufs):
+        assert not b[..., 0].any()
+        want = torch.arange(sum(w[:i]), sum(w[:i + 1]), dtype=torch.int32, device="cuda")
+        assert all(torch.equal(b[n, 0, :, 1], want) for n in range(3))
