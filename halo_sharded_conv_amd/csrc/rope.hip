@@ -42,6 +42,7 @@ struct RopeArgs {
   int32_t turned;                         // the first `turned` pairs rotate
   int32_t vecs;                           // pair vectors of a head: pairs / VEC
   int32_t tb;                             // tokens of a workgroup
+  int32_t block0;                         // this launch's first workgroup
   Div31 by_vecs, by_heads, by_turned;
   float sign;
   double turn[kRopePairs];                // turns per position
@@ -79,7 +80,7 @@ __device__ __forceinline__ void store_pairs(char* p, int a, int b, const float (
 template <class TX, class TO, int VEC, bool ADJ>
 __global__ __launch_bounds__(kRopeThreads) void rope_axes(const RopeArgs a) {
   __shared__ float2 table[kRopeTable];
-  const int t0 = blockIdx.x * a.tb;
+  const int t0 = (a.block0 + (int)blockIdx.x) * a.tb;
   const int nt = min(a.tb, a.tokens - t0);
   for (int i = threadIdx.x; i < nt * a.turned; i += kRopeThreads) {
     const int t = quo(i, a.by_turned), p = i - t * a.turned;
@@ -123,14 +124,20 @@ __global__ __launch_bounds__(kRopeThreads) void rope_axes(const RopeArgs a) {
 }
 
 template <class TX, class TO, int VEC>
-st_status rope_launch(const RopeArgs& a, bool adj, hipStream_t st) {
-  const dim3 grid((a.tokens + a.tb - 1) / a.tb);
-  if (adj) rope_axes<TX, TO, VEC, true><<<grid, kRopeThreads, 0, st>>>(a);
-  else rope_axes<TX, TO, VEC, false><<<grid, kRopeThreads, 0, st>>>(a);
-  return launch_check("rope_axes");
+st_status rope_launch(RopeArgs& a, bool adj, hipStream_t st) {
+  const int64_t blocks = ((int64_t)a.tokens + a.tb - 1) / a.tb;
+  for (int64_t b = 0; b < blocks; b += max_blocks(kRopeThreads)) {
+    a.block0 = (int32_t)b;
+    const dim3 grid((uint32_t)std::min<int64_t>(blocks - b, max_blocks(kRopeThreads)));
+    if (adj) rope_axes<TX, TO, VEC, true><<<grid, kRopeThreads, 0, st>>>(a);
+    else rope_axes<TX, TO, VEC, false><<<grid, kRopeThreads, 0, st>>>(a);
+    const st_status s = launch_check("rope_axes");
+    if (s != ST_OK) return s;
+  }
+  return ST_OK;
 }
 
-template <class TX, class TO> st_status rope_vec(const RopeArgs& a, int vec, bool adj, hipStream_t st) {
+template <class TX, class TO> st_status rope_vec(RopeArgs& a, int vec, bool adj, hipStream_t st) {
   switch (vec) {
     case 4: return rope_launch<TX, TO, 4>(a, adj, st);
     case 2: return rope_launch<TX, TO, 2>(a, adj, st);

@@ -143,3 +143,17 @@ def test_positions_of_more_cells_than_one_launch_holds(gpu_lib):
         assert not b[..., 0].any()
         want = torch.arange(sum(w[:i]), sum(w[:i + 1]), dtype=torch.int32, device="cuda")
         assert all(torch.equal(b[n, 0, :, 1], want) for n in range(3))
+
+
+@pytest.mark.parametrize("tokens_,heads", [(2 ** 31 - 1, 1), ((1 << 24) + 3, 1025)])
+def test_most_tokens(gpu_lib, tokens_, heads):
+    """The most tokens that a call takes, whose number rounded up to whole
+    workgroups passes 31 bits; and 2^24 workgroups, one more than a launch takes."""
+    x = torch.empty(tokens_, heads, 2, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    pos = torch.arange(tokens_, dtype=torch.int32, device="cuda").view(-1, 1)
+    ends = [slice(0, 30), slice((1 << 24) - 20, (1 << 24) + 2), slice(tokens_ - 30, tokens_)]
+    want = [x[e].clone() for e in ends]
+    for w, e in zip(want, ends):
+        gpu_lib.st_rope_axes(w, pos[e].clone(), [2], w)
+    gpu_lib.st_rope_axes(x, pos, [2], x)
+    assert all(torch.equal(x[e], w) for e, w in zip(ends, want))
