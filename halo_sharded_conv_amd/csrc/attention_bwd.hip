@@ -572,16 +572,20 @@ extern "C" st_status st_attention_packed_backward(st_seqs* seqs, const st_tokens
   auto err = [](st_status s, const std::string& m) { return fail(s, "st_attention_packed_backward: " + m); };
   if (!seqs || !q || !k || !v || !out || !dout || !dq || !dk || !dv) return err(ST_ERR_INVALID_ARG, "NULL argument");
   if (!(scale > 0.f) || !std::isfinite(scale)) return err(ST_ERR_INVALID_ARG, "scale must be positive and finite");
-  const int es = seqs->dtype == ST_F32 ? 4 : 2, span = 256;               // rows of the largest tile
+  const int es = seqs->dtype == ST_F32 ? 4 : 2;
+  // tokens of a tile that is read with 31-bit offsets: attn_dq's of k and v,
+  // attn_dkv's of q and dout, and of v where it lies in LDS (wide fp32 heads)
+  const int tile = 64, vtile = seqs->dtype == ST_F32 && seqs->dp > 64 ? 128 : 64;
   const int64_t tq = seqs->total_q, tk = seqs->total_k;
   AttnArgs a{};
-  struct { AttnTensor* t; const st_tokens* v; bool keys; const char* name; } const all[] = {
-      {&a.q, q, false, "st_attention_packed_backward: q"},       {&a.k, k, true, "st_attention_packed_backward: k"},
-      {&a.v, v, true, "st_attention_packed_backward: v"},        {&a.out, out, false, "st_attention_packed_backward: out"},
-      {&a.dout, dout, false, "st_attention_packed_backward: dout"}, {&a.dq, dq, false, "st_attention_packed_backward: dq"},
-      {&a.dk, dk, true, "st_attention_packed_backward: dk"},     {&a.dv, dv, true, "st_attention_packed_backward: dv"}};
+  struct { AttnTensor* t; const st_tokens* v; bool keys; int span; const char* name; } const all[] = {
+      {&a.q, q, false, tile, "st_attention_packed_backward: q"}, {&a.k, k, true, tile, "st_attention_packed_backward: k"},
+      {&a.v, v, true, vtile, "st_attention_packed_backward: v"}, {&a.out, out, false, 1, "st_attention_packed_backward: out"},
+      {&a.dout, dout, false, tile, "st_attention_packed_backward: dout"},
+      {&a.dq, dq, false, 1, "st_attention_packed_backward: dq"}, {&a.dk, dk, true, 1, "st_attention_packed_backward: dk"},
+      {&a.dv, dv, true, 1, "st_attention_packed_backward: dv"}};
   for (const auto& e : all) {
-    const st_status s = attn_tensor(*e.t, e.v, e.keys ? tk : tq, e.keys ? seqs->kv_heads : seqs->heads, seqs->dim, es, span, e.name);
+    const st_status s = attn_tensor(*e.t, e.v, e.keys ? tk : tq, e.keys ? seqs->kv_heads : seqs->heads, seqs->dim, es, e.span, e.name);
     if (s != ST_OK) return s;
   }
   // one group's heads lie within a tile's 31-bit offsets

@@ -723,8 +723,9 @@ size_t st_attention_workspace_bytes(const st_seqs* seqs, int32_t backward);
  * row does not see have no part in it, NaN and infinities included.  The
  * result's bits depend on the plan only, not on timing.
  * Errors: ST_ERR_WORKSPACE, ST_ERR_ALIGNMENT, ST_ERR_BAD_SHAPE (rows that
- * overlap), ST_ERR_UNSUPPORTED (strides past 2^30 bytes a tile; first use inside
- * a graph capture without st_seqs_upload), ST_ERR_INVALID_ARG, ST_ERR_HIP.
+ * overlap), ST_ERR_UNSUPPORTED (64 tokens of k or v, or one of q or out, that span
+ * more than 2^30 bytes; first use inside a graph capture without
+ * st_seqs_upload), ST_ERR_INVALID_ARG, ST_ERR_HIP.
  */
 st_status st_attention_packed(st_seqs* seqs, const st_tokens* q, const st_tokens* k, const st_tokens* v, float scale,
                               const st_tokens* out, float* lse_or_null, void* workspace, size_t workspace_bytes,
@@ -737,6 +738,8 @@ st_status st_attention_packed(st_seqs* seqs, const st_tokens* q, const st_tokens
  *   dq, dk, dv          gradients at q, k, v (written; must not overlap an input);
  *                       dk and dv are summed over the query heads of their group
  *   workspace           >= st_attention_workspace_bytes(seqs, 1) bytes
+ * 64 tokens of q, k, v and dout (128 of v for fp32 heads wider than 64 channels)
+ * and one token of the others may span 2^30 bytes.
  * No atomics: the bits depend on the plan only.  A NaN or infinity in a query,
  * key or value reaches the gradients of its whole sequence, and no other one's.
  */

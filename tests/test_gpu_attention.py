@@ -359,3 +359,32 @@ def test_more_tiles_than_one_launch_holds(gpu_lib):
     assert torch.equal(r["out"], v) and torch.equal(r["dv"], dout)
     assert not r["dq"].any() and not r["dk"].any()
     assert bool(((r["lse"] - 0.3 * (q.float() * k.float()).sum(-1)).abs() < 1e-4).all())
+
+
+@pytest.mark.parametrize("dtype,heads,kv_heads,dim", [("bf16", 4, 2, 64), ("f32", 2, 1, 128), ("f32", 2, 2, 64)])
+def test_token_strides_at_the_limit(gpu_lib, dtype, heads, kv_heads, dim):
+    """Tokens as far apart as both calls take: 16 MiB, 8 MiB of v of wide fp32 heads."""
+    n = 150
+    host = inputs([n], [n], heads, kv_heads, dim, dtype, seed=13)
+    dev = [t.cuda() for t in host]
+    want = run(gpu_lib, *dev, [n], [n], dtype, True, 0.1)
+    es = 2 if dtype == "bf16" else 4
+
+    def far(t, stride, at):
+        big = torch.empty(n * stride // es, dtype=t.dtype, device="cuda")
+        v = big[at:].as_strided(t.shape, (stride // es, dim, 1), at)
+        v.copy_(t)
+        return v
+
+    q, k, v, dout = dev
+    wide = dtype == "f32" and dim > 64
+    q, k, dout = far(q, 1 << 24, 64), far(k, 1 << 24, 0), far(dout, 1 << 24, 128)
+    v = far(v, 1 << 23 if wide else 1 << 24, 0)
+    seqs = gpu_lib.st_plan_sequences([n], [n], heads, kv_heads, dim, dtype, True)
+    ws = torch.empty(gpu_lib.st_attention_workspace_bytes(seqs, True), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(want["out"]), torch.empty_like(want["lse"])
+    gpu_lib.st_attention_packed(seqs, q, k, v, 0.1, out, lse, ws)
+    grads = [torch.empty_like(want[g]) for g in ("dq", "dk", "dv")]
+    gpu_lib.st_attention_packed_backward(seqs, q, k, v, out, lse, dout, 0.1, *grads, ws)
+    for got, name in zip([out, lse] + grads, ("out", "lse", "dq", "dk", "dv")):
+        assert torch.equal(got, want[name]), name

@@ -198,3 +198,30 @@ def test_types_that_are_not_read_as_bits():
     for wrong in (t.float64, t.bfloat16, t.int64):
         assert status(lambda: hsc.st_attention_packed(one, None, None, None, 0.1, None, Device(wrong), stream=0)) == INVALID
         assert status(lambda: hsc.st_attention_packed_backward(one, *[None] * 4, Device(wrong), None, 0.1, *[None] * 4, stream=0)) == INVALID
+
+
+def test_backward_strides():
+    """Token strides up to 2^30 bytes over a tile's tokens pass (the call then
+    lacks its workspace); the outputs' have the forward call's limit."""
+    def back(s, es, **big):
+        q, k = view(1 << 20), view(1 << 20, 128)
+        args = dict(q=q, k=k, v=k, out=q, dout=q, dq=q, dk=k, dv=k)
+        args.update({n: view(1 << 20, t // es) for n, t in big.items()})
+        a = [args[n] for n in ("q", "k", "v", "out")] + [1 << 20, args["dout"], 0.1] + [args[n] for n in ("dq", "dk", "dv")]
+        return lib.st_attention_packed_backward(s.handle, *a, None, 0, None)
+
+    half, single, wide = seqs([8]), seqs([8], dtype="f32"), seqs([8], dim=128, dtype="f32", heads=2, kv=2)
+    for s, es in ((half, 2), (single, 4)):
+        assert back(s, es, **{n: 1 << 24 for n in ("q", "k", "v", "dout")}) == WORKSPACE
+        assert back(s, es, **{n: 1 << 30 for n in ("out", "dq", "dk", "dv")}) == WORKSPACE
+        for n in ("q", "k", "v", "dout"):
+            assert back(s, es, **{n: (1 << 24) + 16}) == UNSUPPORTED, n
+        for n in ("out", "dq", "dk", "dv"):
+            assert back(s, es, **{n: (1 << 30) + 16}) == UNSUPPORTED, n
+    kv = view(1 << 20, 256, 128)
+
+    def wide_v(t):
+        q, v = view(1 << 20, 256, 128), view(1 << 20, t // 4, 128)
+        return lib.st_attention_packed_backward(wide.handle, q, kv, v, q, 1 << 20, q, 0.1, q, kv, kv, None, 0, None)
+
+    assert wide_v(1 << 23) == WORKSPACE and wide_v((1 << 23) + 16) == UNSUPPORTED
