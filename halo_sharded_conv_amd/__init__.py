@@ -620,7 +620,9 @@ __all__ = [
     "st_groupnorm_combine", "st_groupnorm_apply", "st_groupnorm_backward_workspace_bytes",
     "st_groupnorm_backward", "st_conv_wgrad_workspace_bytes", "st_conv_wgrad", "st_plan_pooled",
     "st_pool_sharded", "st_plan_strided", "st_conv_strided_sharded", "st_plan_transposed",
-    "st_conv_transposed_sharded",
+    "st_conv_transposed_sharded", "st_layernorm_sharded", "st_layernorm_backward",
+    "st_layernorm_backward_workspace_bytes", "st_plan_positions", "st_rope_axes", "Sequences", "st_plan_sequences",
+    "st_attention_workspace_bytes", "st_attention_packed", "st_attention_packed_backward",
 ]
 
 

@@ -225,3 +225,11 @@ def test_backward_strides():
         return lib.st_attention_packed_backward(wide.handle, q, kv, v, q, 1 << 20, q, 0.1, q, kv, kv, None, 0, None)
 
     assert wide_v(1 << 23) == WORKSPACE and wide_v((1 << 23) + 16) == UNSUPPORTED
+
+
+def test_every_entry_point_is_exported():
+    """`from halo_sharded_conv_amd import *` brings every function of the binding
+    and the classes they return."""
+    functions = {n for n in vars(hsc) if n.startswith("st_") and callable(getattr(hsc, n))}
+    assert functions | {"Plan", "Sequences"} <= set(hsc.__all__)
+    assert all(hasattr(hsc, n) for n in hsc.__all__)
