@@ -622,7 +622,7 @@ __all__ = [
     "st_pool_sharded", "st_plan_strided", "st_conv_strided_sharded", "st_plan_transposed",
     "st_conv_transposed_sharded", "st_layernorm_sharded", "st_layernorm_backward",
     "st_layernorm_backward_workspace_bytes", "st_plan_positions", "st_rope_axes", "Sequences", "st_plan_sequences",
-    "st_attention_workspace_bytes", "st_attention_packed", "st_attention_packed_backward",
+    "st_attention_workspace_bytes", "st_attention_packed", "st_attention_packed_backward", "st_groupnorm_combine_apply",
 ]
 
 
