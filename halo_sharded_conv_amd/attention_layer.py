@@ -66,7 +66,6 @@ class ShardedAttention:
         plan = lambda c, t: st_plan_shards(nd, batch, c, spatial, shards, [0] * nd, t)  # noqa: E731
         self.x_plan, self.norm_plan = plan(channels, ST_F32), plan(channels, ST_BF16)
         self.joint_plan, self.width_plan = plan(joint, ST_BF16), plan(width, ST_BF16)
-        self.wide_plan = plan(width, ST_F32)
         cells = _cells(self.x_plan)
         self.starts = [sum(cells[:i]) for i in range(len(cells) + 1)]
         self.tokens = t = self.starts[-1]
@@ -159,9 +158,9 @@ class ShardedAttention:
         need = max(st_conv_wgrad_workspace_bytes(self.norm_plan, self.joint_width, 1),
                    st_conv_wgrad_workspace_bytes(self.width_plan, self.channels, 1),
                    st_layernorm_backward_workspace_bytes(self.x_plan), 16)
-        conv = max(st_conv_workspace_bytes(self.norm_plan, self.width, 1),
-                   st_conv_workspace_bytes(self.joint_plan, self.channels, 1))
-        if conv == 0:
+        conv = [st_conv_workspace_bytes(self.norm_plan, self.width, 1),
+                st_conv_workspace_bytes(self.joint_plan, self.channels, 1)]
+        if 0 in conv:
             raise ShardConvError(4, "unsupported channel counts")
         new = lambda *shape, dt=f32: torch.empty(*shape, dtype=dt, device=dev)  # noqa: E731
         g = {"wide": new(t, self.width), "dout": new(t, self.width, dt=bf16), "dqkv": new(t, self.joint_width, dt=bf16),
@@ -169,7 +168,7 @@ class ShardedAttention:
              "dw_qkv": new(self.joint_width, self.channels), "dw_out": new(self.channels, self.width),
              "dgamma": new(self.channels), "dbeta": new(self.channels),
              "wt": new(max(self.w_qkv.numel(), self.w_out.numel()), dt=bf16),
-             "ws": new(need, dt=torch.uint8), "conv_ws": new(conv, dt=torch.uint8)}
+             "ws": new(need, dt=torch.uint8), "conv_ws": new(max(conv), dt=torch.uint8)}
         # Nothing is filled, but the memory may have had another owner, whose work
         # the current stream alone has in order: the steps may run on another.
         if not torch.cuda.is_current_stream_capturing():

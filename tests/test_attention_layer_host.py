@@ -103,3 +103,17 @@ def test_upstream_gradient_of_another_type(events):
         layer.backward(x, torch.zeros(24, 32))
     assert e.value.status == 1 and not [n for n in names(events) if n != "synchronize"]
     layer.backward(x, torch.zeros(24, 32, dtype=torch.int16))  # bf16 bits
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_backward_convs_are_both_checked(events, monkeypatch, which):
+    """An input-gradient conv that the library does not have shows as a
+    workspace of zero bytes, whichever of the two it is."""
+    layer = make()
+    real = [layer.norm_plan, layer.joint_plan]
+    ask = attention_layer.st_conv_workspace_bytes
+    monkeypatch.setattr(attention_layer, "st_conv_workspace_bytes",
+                        lambda plan, *a: 0 if plan is real[which] else ask(plan, *a))
+    with pytest.raises(hsc.ShardConvError) as e:
+        layer.alloc_backward()
+    assert e.value.status == 4 and layer.grads is None
