@@ -737,7 +737,7 @@ def st_rope_axes(x, positions, axis_dims: Sequence[int], out, rotated_heads: Opt
     """Rotary positions with one section of channels per axis.
 
     x, out: [tokens, heads, head_dim], float32 or bfloat16 each, any token and
-    head strides; out may be x.  positions: int32 [tokens, axes].
+    head strides; out may be x.  positions: int32 [tokens, axes] (or flat).
     rotated_heads: heads that turn (default all), the others are copied.
     """
     _rows3(x, "st_rope_axes x")
@@ -750,6 +750,8 @@ def st_rope_axes(x, positions, axis_dims: Sequence[int], out, rotated_heads: Opt
     n = len(axis_dims)
     if positions.dtype != _torch().int32:
         raise ShardConvError(1, "st_rope_axes: positions must be int32")
+    if n and positions.dim() > 1 and positions.shape[-1] != n:
+        raise ShardConvError(2, f"st_rope_axes: positions are {tuple(positions.shape)}, axis_dims names {n} axes")
     pos = _dev_ptr(positions, "positions", 4 * tokens * n)
     dims = (ctypes.c_int32 * max(1, n))(*axis_dims)
     _check(lib.st_rope_axes(x.data_ptr(), _float_dtype(x, "st_rope_axes x"), x.stride(0), x.stride(1), tokens, heads,

@@ -157,3 +157,18 @@ def test_most_tokens(gpu_lib, tokens_, heads):
         gpu_lib.st_rope_axes(w, pos[e].clone(), [2], w)
     gpu_lib.st_rope_axes(x, pos, [2], x)
     assert all(torch.equal(x[e], w) for e, w in zip(ends, want))
+
+
+def test_positions_of_another_number_of_axes(gpu_lib):
+    """Three axes' positions with two sections are refused, not read across rows;
+    grids and flat buffers of the right number pass."""
+    x = torch.randn(6, 2, 64, device="cuda")
+    pos = torch.arange(18, dtype=torch.int32, device="cuda")
+    with pytest.raises(gpu_lib.ShardConvError) as e:
+        gpu_lib.st_rope_axes(x, pos.view(6, 3), [32, 32], x.clone())
+    assert e.value.status == 2
+    outs = [torch.empty_like(x) for _ in range(3)]
+    for o, p in zip(outs, (pos.view(6, 3), pos.view(2, 3, 3), pos)):
+        gpu_lib.st_rope_axes(x, p, [16, 24, 24], o)
+    check(outs[0], x, pos.view(6, 3), [16, 24, 24])
+    assert torch.equal(outs[1], outs[0]) and torch.equal(outs[2], outs[0])

@@ -233,3 +233,32 @@ def test_every_entry_point_is_exported():
     functions = {n for n in vars(hsc) if n.startswith("st_") and callable(getattr(hsc, n))}
     assert functions | {"Plan", "Sequences"} <= set(hsc.__all__)
     assert all(hasattr(hsc, n) for n in hsc.__all__)
+
+
+def test_positions_are_not_read_across_rows():
+    """[tokens, 3] positions with two sections."""
+    t = hsc._torch()
+
+    class Rows(Device):
+        def __init__(self, dtype, *shape):
+            super().__init__(dtype)
+            self.shape = shape
+
+        def dim(self):
+            return len(self.shape)
+
+        def numel(self):
+            return 1
+
+        def stride(self, i):
+            return (128, 64, 1)[i]
+
+    x = Rows(t.float32, 6, 2, 64)
+
+    def status(*shape):
+        with pytest.raises(hsc.ShardConvError) as e:
+            hsc.st_rope_axes(x, Rows(t.int32, *shape), [32, 32], x, stream=0)
+        return e.value.status
+
+    assert status(6, 3) == BAD_SHAPE and status(6, 1) == BAD_SHAPE and status(2, 3, 3) == BAD_SHAPE
+    assert status(6, 2) == ALIGN and status(12) == ALIGN and status(2, 3, 2) == ALIGN
