@@ -119,11 +119,20 @@ class ShardedAttention:
         Waits for the device before and after: steps on any stream see one set
         of weights."""
         torch = _torch()
+
+        def put(name, a, to, *shape):
+            if a is None:
+                return None
+            a = np.ascontiguousarray(a, np.float32)
+            if a.size != to.numel() or (a.ndim > 1 and a.shape[:len(shape)] != shape):
+                raise ShardConvError(2, f"{name}: expected {shape}, got {a.shape}")
+            return to.copy_(torch.from_numpy(a.reshape(-1)))
+
         torch.cuda.synchronize()
-        self.w_qkv.copy_(torch.from_numpy(np.ascontiguousarray(w_qkv, np.float32).reshape(-1)))
-        self.w_out.copy_(torch.from_numpy(np.ascontiguousarray(w_out, np.float32).reshape(-1)))
-        put = lambda a, to: None if a is None else to.copy_(torch.from_numpy(np.asarray(a, np.float32).reshape(to.shape)))  # noqa: E731
-        self.gamma, self.beta = put(gamma, self._gamma), put(beta, self._beta)
+        put("w_qkv", w_qkv, self.w_qkv, self.joint_width, self.channels)
+        put("w_out", w_out, self.w_out, self.channels, self.width)
+        self.gamma = put("gamma", gamma, self._gamma, self.channels)
+        self.beta = put("beta", beta, self._beta, self.channels)
         torch.cuda.synchronize()
 
     # ------------------------------------------------------------- steps

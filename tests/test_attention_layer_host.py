@@ -117,3 +117,15 @@ def test_backward_convs_are_both_checked(events, monkeypatch, which):
     with pytest.raises(hsc.ShardConvError) as e:
         layer.alloc_backward()
     assert e.value.status == 4 and layer.grads is None
+
+
+def test_weights_of_another_shape(events):
+    """A transposed matrix has the right size and the wrong meaning."""
+    layer = make()
+    w_qkv, w_out = np.ones((64, 32)), np.ones((32, 32))
+    layer.set_weights(w_qkv.reshape(64, 32, 1, 1), w_out.reshape(-1))
+    for bad in (dict(w_qkv=w_qkv.T), dict(w_qkv=np.ones((64, 31))), dict(w_out=np.ones(1)), dict(gamma=np.ones(31)),
+                dict(beta=np.ones(1))):
+        with pytest.raises(hsc.ShardConvError) as e:
+            layer.set_weights(**{**dict(w_qkv=w_qkv, w_out=w_out), **bad})
+        assert e.value.status == 2, bad
