@@ -242,6 +242,9 @@ st_status st_rope_axes(const void* x, st_dtype x_dtype, int64_t x_token_stride, 
     sum += axis_dims[i];
   }
   if (sum > head_dim) return err(ST_ERR_BAD_SHAPE, "axis widths add up to more than head_dim");
+  // one token or one head has no stride: any value stands for it
+  if (tokens == 1) x_token_stride = out_token_stride = 0;
+  if (heads == 1) x_head_stride = out_head_stride = 0;
   if (x_token_stride < 0 || x_head_stride < 0 || out_token_stride < 0 || out_head_stride < 0)
     return err(ST_ERR_INVALID_ARG, "negative stride");
   if (heads > 65536 || tokens >= (1ll << 31)) return err(ST_ERR_UNSUPPORTED, "too many heads or tokens");

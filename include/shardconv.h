@@ -646,7 +646,8 @@ st_status st_plan_positions(const st_plan* plan, int32_t* const* pos_bufs, void*
  * positions[token][a] * base^(-2 i / axis_dims[a]):
  *   (u, v) -> (u cos - v sin, u sin + v cos)
  *   x, x_dtype          input; head h of token t starts at element
- *                       t * x_token_stride + h * x_head_stride
+ *                       t * x_token_stride + h * x_head_stride (of one token or
+ *                       one head the stride is not looked at)
  *   tokens              >= 0 (0: nothing is done), below 2^31
  *   rotated_heads       heads below this one turn, the others are copied (a joint
  *                       q, k, v projection turns q and k and copies v)

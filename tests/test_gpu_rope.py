@@ -172,3 +172,23 @@ def test_positions_of_another_number_of_axes(gpu_lib):
         gpu_lib.st_rope_axes(x, p, [16, 24, 24], o)
     check(outs[0], x, pos.view(6, 3), [16, 24, 24])
     assert torch.equal(outs[1], outs[0]) and torch.equal(outs[2], outs[0])
+
+
+@pytest.mark.parametrize("pairs", ["halves", "adjacent"])
+def test_one_token_or_one_head_has_no_stride(gpu_lib, pairs):
+    """Whatever stride a view names for it, odd or other than the output's."""
+    rng = np.random.default_rng(5)
+    x = torch.from_numpy(rng.normal(size=(4, 4, 64))).bfloat16().cuda()
+    pos = torch.from_numpy(rng.integers(0, 99, size=(4, 2))).to(torch.int32).cuda()
+    for tokens_, heads, strides in ((1, 4, (65, 64, 1)), (4, 1, (256, 3, 1)), (1, 1, (7, 9, 1))):
+        p, src = pos[:tokens_].contiguous(), x[:tokens_, :heads].contiguous()
+        want = torch.empty_like(src)
+        gpu_lib.st_rope_axes(src, p, [32, 32], want, pairs=pairs)
+        check(want, src, p, [32, 32], pairs=pairs)
+        v = x.clone().as_strided((tokens_, heads, 64), strides)
+        same = v.as_strided((tokens_, heads, 64), (256, 64, 1))
+        out = torch.empty_like(want)
+        gpu_lib.st_rope_axes(v, p, [32, 32], out, pairs=pairs)
+        assert torch.equal(out, want)
+        gpu_lib.st_rope_axes(v, p, [32, 32], same, pairs=pairs)   # in place, under other strides
+        assert torch.equal(same, want)
