@@ -388,3 +388,50 @@ def test_token_strides_at_the_limit(gpu_lib, dtype, heads, kv_heads, dim):
     gpu_lib.st_attention_packed_backward(seqs, q, k, v, out, lse, dout, 0.1, *grads, ws)
     for got, name in zip([out, lse] + grads, ("out", "lse", "dq", "dk", "dv")):
         assert torch.equal(got, want[name]), name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("q_lens,k_lens,heads,kv_heads,dim", [
+    ([130], [3000], 2, 1, 96), ([130], [3000], 2, 2, 128), ([140], [1700], 1, 1, 72),     # keys split for out and dq
+    ([1, 20], [900, 2500], 4, 2, 96), ([2], [3000], 3, 1, 128),                           # one-wave tiles
+    ([3000], [130], 1, 1, 96), ([1500], [20], 2, 1, 128),                                 # rows split for dk and dv
+])
+def test_split_work_of_wide_heads(gpu_lib, q_lens, k_lens, heads, kv_heads, dim, causal, dtype):
+    say(f"split attention {dtype} {heads}/{kv_heads} x {dim} causal={causal} q={q_lens} k={k_lens}")
+    host = inputs(q_lens, k_lens, heads, kv_heads, dim, dtype, seed=14)
+    dev = [t.cuda() for t in host]
+    seqs = gpu_lib.st_plan_sequences(q_lens, k_lens, heads, kv_heads, dim, dtype, causal)
+    if not causal or max(q_lens) <= max(k_lens):           # (few rows see a key otherwise)
+        assert gpu_lib.st_attention_workspace_bytes(seqs, backward=True) > 4 * sum(q_lens) * heads + 256   # partial results
+    r = run(gpu_lib, *dev, q_lens, k_lens, dtype, causal, dim ** -0.5)
+    check(r, *host, q_lens, k_lens, dtype, causal, dim ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lq,lk,at", [(130, 1500, 300), (130, 1500, 1450), (3, 2000, 700), (600, 600, 290)])
+def test_special_values_in_split_and_whole_tiles(gpu_lib, dtype, lq, lk, at):
+    """A NaN or infinite value of a key in a tile that every row sees, in a masked
+    one of a split row, and a NaN in K, with the scores too close together for any
+    weight to underflow: what the rows that see the key get, and no other."""
+    heads, kv_heads, dim = 4, 2, 64
+    group, first = heads // kv_heads, max(0, at - (lk - lq))
+    host = inputs([lq], [lk], heads, kv_heads, dim, dtype, seed=15)
+    clean = run(gpu_lib, *[t.cuda() for t in host], [lq], [lk], dtype, True, 0.05, train=False)
+    for where in ("k", "v"):
+        for value in (math.nan, math.inf, -math.inf):
+            if where == "k" and not math.isnan(value):
+                continue
+            bad = [t.clone() for t in host]
+            bad["qkv".index(where)][at, 0, 5] = value
+            r = run(gpu_lib, *[t.cuda() for t in bad], [lq], [lk], dtype, True, 0.05, train=False)
+            assert torch.equal(r["out"][:first], clean["out"][:first])
+            assert torch.equal(r["out"][:, group:], clean["out"][:, group:])
+            if where == "k":
+                assert bool(torch.isnan(r["out"][first:, :group].float()).all())
+                continue
+            got = r["out"][first:, :group, 5].float()
+            assert bool((torch.isnan(got) if math.isnan(value) else got == value).all()), value
+            rest = r["out"].clone()
+            rest[first:, :group, 5] = clean["out"][first:, :group, 5]
+            assert torch.equal(rest, clean["out"])
