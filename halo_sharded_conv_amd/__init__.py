@@ -165,8 +165,7 @@ class Plan:
         self.ndim, self.batch, self.channels, self.dtype = ndim, batch, channels, dtype
         self.shards = tuple(tuple(s) for s in shards)
         self.halo = tuple(halo)
-        self._bytes = None
-        self._cells = None
+        self._bytes = self._cells = self._stats = None
 
     @property
     def handle(self) -> ctypes.c_void_p:
@@ -640,16 +639,23 @@ _TYPES = {ST_F32: _FP32, ST_BF16: _bits("bfloat16", "int16", "uint8")}
 
 def _typed(t, what: str, types, min_bytes: int = 0) -> int:
     """_dev_ptr of a tensor of one of these types, or of None."""
-    if t is not None and getattr(t, "is_cuda", False) and t.dtype not in types:
+    if t is not None and getattr(t, "is_cuda", False) and t.dtype in types and t.is_contiguous() and t.nbytes >= min_bytes:
+        return t.data_ptr()
+    ptr = _dev_ptr(t, what, min_bytes)       # its message, or the dtype's
+    if t is not None:
         raise ShardConvError(1, f"{what}: unexpected dtype {t.dtype}")
-    return _dev_ptr(t, what, min_bytes)
+    return ptr
 
 
 def _typed_array(tensors, what: str, types, sizes: List[int]):
-    arr = _ptr_array(tensors, what, sizes)
+    if len(tensors) != len(sizes):
+        return _ptr_array(tensors, what, sizes)   # its message
+    arr = (ctypes.c_void_p * max(1, len(sizes)))()
     for i, t in enumerate(tensors):
-        if t is not None and t.dtype not in types:
-            raise ShardConvError(1, f"{what}[{i}]: unexpected dtype {t.dtype}")
+        if t is not None and getattr(t, "is_cuda", False) and t.dtype in types and t.is_contiguous() and t.nbytes >= sizes[i]:
+            arr[i] = t.data_ptr()
+        else:
+            arr[i] = _typed(t, f"{what}[{i}]", types, sizes[i])   # its message
     return arr
 
 
@@ -671,6 +677,13 @@ def _cells(plan: Plan) -> List[int]:
     return plan._cells
 
 
+def _stats_bytes(plan: Plan) -> int:
+    """Of the layer norm's statistics: 2 floats per cell."""
+    if plan._stats is None:
+        plan._stats = 8 * sum(_cells(plan))
+    return plan._stats
+
+
 def st_layernorm_sharded(x_plan: Plan, x_bufs, gamma, beta, eps: float, y_plan: Plan, y_bufs, stats=None,
                          stream=None) -> None:
     """Layer norm over the channels of every cell; stats: 2 floats per cell
@@ -679,7 +692,7 @@ def st_layernorm_sharded(x_plan: Plan, x_bufs, gamma, beta, eps: float, y_plan: 
     ys = _plan_array(y_plan, y_bufs, "st_layernorm_sharded y")
     g = _typed(gamma, "gamma", _FP32, 4 * x_plan.channels)
     b = _typed(beta, "beta", _FP32, 4 * x_plan.channels)
-    st = _typed(stats, "stats", _FP32, 8 * sum(_cells(x_plan)))
+    st = _typed(stats, "stats", _FP32, _stats_bytes(x_plan))
     _check(lib.st_layernorm_sharded(x_plan.handle, xs, g, b, float(eps), y_plan.handle, ys, st, _stream(stream)),
            "st_layernorm_sharded")
 
@@ -697,7 +710,7 @@ def st_layernorm_backward(x_plan: Plan, x_bufs, dy_plan: Plan, dy_bufs, gamma, s
     c = 4 * x_plan.channels
     ws, nb = _ws(workspace)
     _check(lib.st_layernorm_backward(x_plan.handle, xs, dy_plan.handle, dys, _typed(gamma, "gamma", _FP32, c),
-                                     _typed(stats, "stats", _FP32, 8 * sum(_cells(x_plan))), dx_plan.handle, dxs,
+                                     _typed(stats, "stats", _FP32, _stats_bytes(x_plan)), dx_plan.handle, dxs,
                                      _typed(dgamma, "dgamma", _FP32, c), _typed(dbeta, "dbeta", _FP32, c), ws, nb,
                                      _stream(stream)), "st_layernorm_backward")
 
