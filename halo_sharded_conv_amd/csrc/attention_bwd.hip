@@ -137,8 +137,9 @@ __global__ __launch_bounds__(64 * NW, (dq_waves<T, DP>())) void attn_dq(const At
         if (b == 0 && j0 == 0) {
           // A row with all its keys in these 32 takes D as the sum of p dp in
           // fp32: `out` is rounded to its type, and with few keys that rounding
-          // is as large as all others together.  A single key weighs exactly one,
-          // so that nothing is left of dq and dk.
+          // is as large as all others together.  (32: the block of scores that a lane
+          // pair holds at once; more keys would need a pass before the first ds.)  A
+          // single key weighs exactly one, so that nothing is left of dq and dk.
           float d = (limit == 1 ? 1.f : s[0]) * dp[0];
 #pragma unroll
           for (int r = 1; r < 16; ++r) d = fmaf(s[r], dp[r], d);

@@ -12,9 +12,10 @@
 // Bound: HBM.  Forward reads x and writes y once, backward reads x and dy and
 // writes dx once; a cell stays in registers between its load and its store,
 // so the variance is the centred one (two passes over registers, none over
-// memory).  A cell is held by `lpr` lanes (a power of two, so sums cross
-// lanes by DPP and swaps), or by the 256 threads of a workgroup when it is
-// wider than a wave holds.  All sums and statistics are fp32.  Measured: 2048^2
+// memory; the backward pass of 4097 to 16383 channels off the 4-grid alone
+// spills, 92 to 596 bytes a lane).  A cell is held by `lpr` lanes (a power of
+// two, so sums cross lanes by DPP and swaps), or by the 256 threads of a
+// workgroup when it is wider than ln_pick lets a wave hold.  All sums and statistics are fp32.  Measured: 2048^2
 // cells of 64 channels in bf16 forward 182 us (5.9 TB/s), backward 322 us (5.0);
 // 1024 x 1792 of 256, fp32 in and bf16 out, 460 us (6.1) and 907 us (5.2), where
 // a large copy moves 4.8.
@@ -332,9 +333,10 @@ struct LnPick {                       // how a cell is held
   bool block;
 };
 
-// Rows per pass and lane layout: the widest vector that divides C, whole
-// cells per wave while a lane holds at most 8 (forward) or 2 (backward: x, dy
-// and both column sums) vectors.
+// Rows per pass and lane layout: the widest vector that divides C, whole cells
+// per wave while a lane holds at most 8 vectors (16 single values) forward, 16
+// values backward (x, dy, gamma and both column sums): up to 4096 channels at 8
+// values a vector, 2048 at 4, 1024 at 1 forward, 1024 backward.
 LnPick ln_pick(int C, bool wide, bool backward) {
   LnPick p{};
   p.vec = C % 8 == 0 && wide ? 8 : C % 4 == 0 ? 4 : 1;

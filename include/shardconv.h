@@ -721,8 +721,9 @@ size_t st_attention_workspace_bytes(const st_seqs* seqs, int32_t backward);
  * A row that sees no key gives zeros and lse = -inf.  bf16 operands multiply on
  * the matrix cores with fp32 accumulation (the weights rounded to bf16), fp32
  * operands in fp32; scores, softmax statistics and sums are fp32.  Keys that a
- * row does not see have no part in it, NaN and infinities included.  The
- * result's bits depend on the plan only, not on timing.
+ * row does not see have no part in it, NaN and infinities included.  An infinite
+ * value that a row does see with a weight below fp32's range gives infinity or
+ * NaN, by where the key lies in the tiles.  The result's bits depend on the plan only, not on timing.
  * Errors: ST_ERR_WORKSPACE, ST_ERR_ALIGNMENT, ST_ERR_BAD_SHAPE (rows that
  * overlap), ST_ERR_UNSUPPORTED (64 tokens of k or v, or one of q or out, that span
  * more than 2^30 bytes; first use inside a graph capture without
@@ -742,7 +743,7 @@ st_status st_attention_packed(st_seqs* seqs, const st_tokens* q, const st_tokens
  * 64 tokens of q, k, v and dout (128 of v for fp32 heads wider than 64 channels)
  * and one token of the others may span 2^30 bytes.
  * No atomics: the bits depend on the plan only.  A NaN or infinity in a query,
- * key or value reaches the gradients of its whole sequence, and no other one's.
+ * key, value or dout reaches the gradients of its whole sequence, and no other one's.
  */
 st_status st_attention_packed_backward(st_seqs* seqs, const st_tokens* q, const st_tokens* k, const st_tokens* v,
                                        const st_tokens* out, const float* lse, const st_tokens* dout, float scale,
