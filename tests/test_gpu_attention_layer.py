@@ -146,3 +146,40 @@ def test_odd_shards(gpu_lib, spatial, shards):
     want = reference(layer, x.astype(np.float64), pos, w_qkv, w_out, gamma, beta, dy, [t])
     errs = {n: off(got[n].double().cpu().numpy().reshape(want[n].shape), want[n]) for n in want}
     assert all(e < 0.02 for e in errs.values()), errs
+
+
+@pytest.mark.parametrize("eager_backward", [True, False])
+def test_captured_branch(gpu_lib, eager_backward):
+    """Forward and backward in one graph, its buffers allocated before or inside
+    the capture: every replay gives the eager bits, with weights set in between."""
+    from halo_sharded_conv_amd.attention_layer import ShardedAttention
+    rng = np.random.default_rng(4)
+    weights = [(rng.normal(size=(4 * 16 + 2 * 2 * 16, 32)) / 6, rng.normal(size=(32, 64)) / 8,
+                1 + 0.2 * rng.normal(size=32), 0.2 * rng.normal(size=32)) for _ in range(2)]
+    x = torch.from_numpy(np.float32(rng.normal(size=(60, 32)))).cuda()
+    dy = torch.from_numpy(rng.normal(size=(60, 32))).bfloat16().cuda()
+
+    def make():
+        layer = ShardedAttention((6, 10), ((2, 4), (10,)), 32, 4, 2, 16)
+        layer.set_weights(*weights[0])
+        return layer
+
+    layer, eager = make(), make()
+    layer.forward(x)
+    if eager_backward:
+        layer.backward(x, dy)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer.forward(x)
+        grads = layer.backward(x, dy)
+    for i in range(4):
+        for one in (layer, eager):
+            one.set_weights(*weights[i % 2])
+        want = {"y": eager.forward(x), **eager.backward(x, dy)}
+        for t in (layer.y, *grads.values()):
+            t.fill_(float(i))
+        g.replay()
+        torch.cuda.synchronize()
+        for n, t in {"y": layer.y, **grads}.items():
+            assert torch.equal(t, want[n]), (i, n)
