@@ -47,6 +47,11 @@ class _Tokens(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("stride", ctypes.c_int64),
+                ("scale_stride", ctypes.c_int64), ("type", ctypes.c_int32)]
+
+
 class _GnLayout(ctypes.Structure):
     _fields_ = [("partials_offset", ctypes.c_size_t), ("stats_offset", ctypes.c_size_t),
                 ("scales_offset", ctypes.c_size_t), ("ymax_offset", ctypes.c_size_t),
@@ -76,7 +81,7 @@ def _load() -> ctypes.CDLL:
         raise ImportError(f"two HIP runtimes are loaded ({runtimes}); import torch before any other HIP library")
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     PP = ctypes.POINTER(ctypes.c_void_p)
-    PI32, PT = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(_Tokens)
+    PI32, PT, PR = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(_Tokens), ctypes.POINTER(_Rows)
     sig = {
         "st_version": (ctypes.c_char_p, []),
         "st_last_error": (ctypes.c_char_p, []),
@@ -132,6 +137,14 @@ def _load() -> ctypes.CDLL:
         "st_attention_workspace_bytes": (SZ, [P, I32]),
         "st_attention_packed": (I32, [P, PT, PT, PT, ctypes.c_float, PT, P, P, SZ, P]),
         "st_attention_packed_backward": (I32, [P, PT, PT, PT, PT, P, PT, ctypes.c_float, PT, PT, PT, P, SZ, P]),
+        "st_mx8_store": (I32, [I64, I64, PR, PR, P]),
+        "st_mx8_load": (I32, [I64, I64, PR, I32, PR, P]),
+        "st_rmsnorm": (I32, [I64, I64, PR, PR, P, ctypes.c_float, PR, PR, PR, P, P]),
+        "st_rmsnorm_backward_workspace_bytes": (SZ, [I64, I64]),
+        "st_rmsnorm_backward": (I32, [I64, I64, PR, PR, PR, P, P, PR, P, P, SZ, P]),
+        "st_linear_workspace_bytes": (SZ, [I64, I64, I64, I32, I32]),
+        "st_linear": (I32, [I64, I64, I64, PR, PR, P, I32, PR, PR, PR, P, SZ, P]),
+        "st_linear_backward": (I32, [I64, I64, I64, PR, PR, I32, PR, PR, PR, PR, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -622,6 +635,8 @@ __all__ = [
     "st_conv_transposed_sharded", "st_layernorm_sharded", "st_layernorm_backward",
     "st_layernorm_backward_workspace_bytes", "st_plan_positions", "st_rope_axes", "Sequences", "st_plan_sequences",
     "st_attention_workspace_bytes", "st_attention_packed", "st_attention_packed_backward", "st_groupnorm_combine_apply",
+    "ST_MX8", "Mx8", "mx8_empty", "st_mx8_store", "st_mx8_load", "st_rmsnorm", "st_rmsnorm_backward_workspace_bytes",
+    "st_rmsnorm_backward", "st_linear_workspace_bytes", "st_linear", "st_linear_backward",
 ]
 
 
@@ -870,3 +885,157 @@ def st_attention_packed_backward(seqs: Sequences, q, k, v, out, lse, dout, scale
         view(dout, "st_attention_packed_backward dout", False), scale, view(dq, "st_attention_packed_backward dq", False),
         view(dk, "st_attention_packed_backward dk", True), view(dv, "st_attention_packed_backward dv", True), ws, nb,
         _stream(stream)), what)
+
+
+# ------------------------------------------- MLP branch: rows of channels, 8 bits
+
+ST_MX8 = 2
+_ROW_TYPES = {"f32": ST_F32, "bf16": ST_BF16, "mx8": ST_MX8}
+_ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+
+
+class Mx8:
+    """Rows of `channels` values in the 8-bit form: codes (bytes, [rows, at least
+    channels]) and scales (bytes, [rows, at least a byte per 32 channels]).  The
+    codes' row stride is a multiple of 16, the scales' of 4."""
+
+    def __init__(self, codes, scales, channels: int):
+        self.codes, self.scales, self.channels = codes, scales, int(channels)
+        blocks = -(-self.channels // 32)
+        for t, what, least in ((codes, "codes", self.channels), (scales, "scales", blocks)):
+            if t.dim() != 2 or t.element_size() != 1 or t.shape[1] < least or (t.shape[1] > 1 and t.numel() and t.stride(1) != 1):
+                raise ShardConvError(2, f"Mx8: {what} are not bytes [rows, >= {least}] with contiguous rows")
+        if codes.shape[0] != scales.shape[0]:
+            raise ShardConvError(2, f"Mx8: {codes.shape[0]} rows of codes and {scales.shape[0]} of scales")
+
+    @property
+    def rows(self) -> int:
+        return int(self.codes.shape[0])
+
+
+def mx8_empty(rows: int, channels: int, device: str = "cuda") -> Mx8:
+    """An unwritten Mx8 whose strides every operator takes."""
+    torch = _torch()
+    return Mx8(torch.empty(rows, -(-channels // 16) * 16, dtype=torch.uint8, device=device),
+               torch.empty(rows, -(-channels // 128) * 4, dtype=torch.uint8, device=device), channels)
+
+
+_ROW_DTYPES = {_torch().float32: ST_F32, _torch().bfloat16: ST_BF16}
+
+
+def _here(t, what: str) -> None:
+    """The kernels run on the current device: operands of another one are refused."""
+    if not getattr(t, "is_cuda", False):
+        raise ShardConvError(1, f"{what}: expected a GPU tensor (no CPU fallback exists)")
+    if t.get_device() != _torch()._C._cuda_getDevice():
+        raise ShardConvError(1, f"{what}: on device {t.get_device()}, which is not the current one")
+
+
+def _rows(t, what: str, rows: int, channels: int):
+    """st_rows of a [rows, channels] tensor or an Mx8; None stays None."""
+    if t is None:
+        return None
+    if isinstance(t, Mx8):
+        if (t.rows, t.channels) != (rows, channels):
+            raise ShardConvError(2, f"{what}: expected {(rows, channels)}, got {(t.rows, t.channels)}")
+        _here(t.codes, what)
+        _here(t.scales, what)
+        return _Rows(t.codes.data_ptr(), t.scales.data_ptr(), t.codes.stride(0), t.scales.stride(0), ST_MX8)
+    _here(t, what)
+    if t.shape != (rows, channels):
+        raise ShardConvError(2, f"{what}: expected {(rows, channels)}, got {tuple(t.shape)}")
+    dt = _ROW_DTYPES.get(t.dtype)
+    if dt is None:
+        raise ShardConvError(1, f"{what}: expected float32, bfloat16 or Mx8, got {t.dtype}")
+    st, sc = t.stride()
+    if sc != 1 and channels > 1 and rows:
+        raise ShardConvError(2, f"{what}: channels must be contiguous")
+    return _Rows(t.data_ptr(), None, st, 0, dt)
+
+
+def _shape(t, what: str):
+    if isinstance(t, Mx8):
+        return t.rows, t.channels
+    if t is None or getattr(t, "dim", lambda: 0)() != 2:
+        raise ShardConvError(2, f"{what}: expected [rows, channels]")
+    return t.shape[0], t.shape[1]
+
+
+def _act(act: str, what: str) -> int:
+    if act not in _ACTS:
+        raise ShardConvError(1, f"{what}: unknown activation {act!r}")
+    return _ACTS[act]
+
+
+def st_mx8_store(x, out: Mx8, stream=None) -> None:
+    """x: [rows, channels], float32 or bfloat16, into the 8-bit form."""
+    n, c = _shape(x, "st_mx8_store x")
+    _check(lib.st_mx8_store(n, c, _rows(x, "st_mx8_store x", n, c), _rows(out, "st_mx8_store out", n, c), _stream(stream)),
+           "st_mx8_store")
+
+
+def st_mx8_load(x: Mx8, out, act: str = "none", stream=None) -> None:
+    """act(x) into [rows, channels], float32 or bfloat16."""
+    n, c = _shape(x, "st_mx8_load x")
+    _check(lib.st_mx8_load(n, c, _rows(x, "st_mx8_load x", n, c), _act(act, "st_mx8_load"),
+                           _rows(out, "st_mx8_load out", n, c), _stream(stream)), "st_mx8_load")
+
+
+def st_rmsnorm(x, residual, gamma, eps: float, total=None, y=None, y8: Optional[Mx8] = None, rstd=None, stream=None) -> None:
+    """s = x + residual (None: x) into total, s * rstd * gamma into y and y8 (the
+    8-bit form); rows of channels in float32 or bfloat16; gamma: C floats or
+    None; rstd: a float per row or None."""
+    what = "st_rmsnorm"
+    n, c = _shape(x, "st_rmsnorm x")
+    _check(lib.st_rmsnorm(n, c, _rows(x, "st_rmsnorm x", n, c), _rows(residual, "st_rmsnorm residual", n, c),
+                          _typed(gamma, "gamma", _FP32, 4 * c), float(eps), _rows(total, "st_rmsnorm total", n, c),
+                          _rows(y, "st_rmsnorm y", n, c), _rows(y8, "st_rmsnorm y8", n, c),
+                          _typed(rstd, "rstd", _FP32, 4 * n), _stream(stream)), what)
+
+
+def st_rmsnorm_backward_workspace_bytes(rows: int, channels: int) -> int:
+    return int(lib.st_rmsnorm_backward_workspace_bytes(rows, channels))
+
+
+def st_rmsnorm_backward(s, dy, dtotal, gamma, rstd, dx, dgamma, workspace, stream=None) -> None:
+    """s: the forward call's total (a tensor, or the Mx8 it was kept in); dtotal:
+    gradient at s from the residual stream, or None; dgamma: C floats or None."""
+    what = "st_rmsnorm_backward"
+    n, c = _shape(s, "st_rmsnorm_backward s")
+    ws, nb = _ws(workspace)
+    _check(lib.st_rmsnorm_backward(n, c, _rows(s, "st_rmsnorm_backward s", n, c), _rows(dy, "st_rmsnorm_backward dy", n, c),
+                                   _rows(dtotal, "st_rmsnorm_backward dtotal", n, c), _typed(gamma, "gamma", _FP32, 4 * c),
+                                   _typed(rstd, "rstd", _FP32, 4 * n), _rows(dx, "st_rmsnorm_backward dx", n, c),
+                                   _typed(dgamma, "dgamma", _FP32, 4 * c), ws, nb, _stream(stream)), what)
+
+
+def st_linear_workspace_bytes(rows: int, channels_in: int, channels_out: int, dtype, backward: bool = False) -> int:
+    """dtype: 'f32', 'bf16' or 'mx8' of the products."""
+    return int(lib.st_linear_workspace_bytes(rows, channels_in, channels_out, _ROW_TYPES.get(dtype, dtype), int(bool(backward))))
+
+
+def st_linear(x, w, bias, y, act: str = "none", residual=None, pre=None, workspace=None, stream=None) -> None:
+    """y = act(x w^T + bias) + residual.  x: [rows, in], w: [out, in], both of one
+    type (float32, bfloat16, Mx8); y, pre: [rows, out] in any of the three, pre
+    receives x w^T + bias; bias: float32 [out] or None."""
+    what = "st_linear"
+    n, k = _shape(x, "st_linear x")
+    m = _shape(w, "st_linear w")[0]
+    ws, nb = _ws(workspace)
+    _check(lib.st_linear(n, k, m, _rows(x, "st_linear x", n, k), _rows(w, "st_linear w", m, k),
+                         _typed(bias, "bias", _FP32, 4 * m), _act(act, what), _rows(residual, "st_linear residual", n, m),
+                         _rows(y, "st_linear y", n, m), _rows(pre, "st_linear pre", n, m), ws, nb, _stream(stream)), what)
+
+
+def st_linear_backward(x, w, dy, dx, dw, dbias, act: str = "none", pre=None, workspace=None, stream=None) -> None:
+    """Gradients of st_linear at x, w and bias (each None: not computed).  x: w's
+    type, or the Mx8 it was kept in; pre: as st_linear wrote it."""
+    what = "st_linear_backward"
+    n, k = _shape(x, "st_linear_backward x")
+    m = _shape(w, "st_linear_backward w")[0]
+    ws, nb = _ws(workspace)
+    _check(lib.st_linear_backward(n, k, m, _rows(x, "st_linear_backward x", n, k), _rows(w, "st_linear_backward w", m, k),
+                                  _act(act, what), _rows(pre, "st_linear_backward pre", n, m),
+                                  _rows(dy, "st_linear_backward dy", n, m), _rows(dx, "st_linear_backward dx", n, k),
+                                  _rows(dw, "st_linear_backward dw", m, k), _typed(dbias, "dbias", _FP32, 4 * m), ws, nb,
+                                  _stream(stream)), what)

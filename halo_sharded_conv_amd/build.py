@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libshardconv.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["plan.cpp", "halo.hip", "conv.hip", "wgrad.hip", "groupnorm.hip", "pool.hip", "strided.hip",
-           "layernorm.hip", "rope.hip", "sequences.cpp", "attention.hip", "attention_bwd.hip"]
+           "layernorm.hip", "rope.hip", "sequences.cpp", "attention.hip", "attention_bwd.hip", "mx8.hip", "rmsnorm.hip", "linear.hip", "linear_api.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -750,6 +750,145 @@ st_status st_attention_packed_backward(st_seqs* seqs, const st_tokens* q, const 
                                        const st_tokens* dq, const st_tokens* dk, const st_tokens* dv, void* workspace,
                                        size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------- rows of channels, 8 bits */
+
+/*
+ * st_rows - one operand of the MLP branch's operators: rows (tokens, cells, a
+ * weight's outputs) of contiguous channels.
+ *   type           ST_F32, ST_BF16, or ST_MX8: 8-bit codes with a power of two per
+ *                  block of ST_MX_BLOCK channels (the OCP microscaling form that
+ *                  gfx950's scaled matrix instructions take).  The value of a
+ *                  channel is its e4m3 code times 2^(scale - 127)
+ *   data           16-byte aligned
+ *   stride         elements from one row to the next: a multiple of 16 bytes, or
+ *                  the row's own length (rows back to back; not for ST_MX8)
+ *   scales         ST_MX8: one byte per block of a row, 16-byte aligned (the last
+ *                  block may be short)
+ *   scale_stride   bytes from one row's scales to the next's: a multiple of 4
+ * Of one row the strides are not looked at.  What lies between a row's end and
+ * the next row is neither used nor written.
+ */
+#define ST_MX_BLOCK 32
+#define ST_MX8 2
+typedef struct st_rows {
+  void* data;
+  uint8_t* scales;
+  int64_t stride, scale_stride;
+  int32_t type;
+} st_rows;
+
+/* Activations: z, max(z, 0), z * Phi(z) (Phi: the normal distribution), z / (1 + exp(-z)). */
+#define ST_ACT_NONE 0
+#define ST_ACT_RELU 1
+#define ST_ACT_GELU 2
+#define ST_ACT_SILU 3
+
+/*
+ * st_mx8_store - rows in fp32 or bf16 to the 8-bit form: activations kept until
+ * the backward pass, weights and inputs of an 8-bit product.
+ *   rows, channels   rows >= 0 (0: nothing is done), channels >= 1, both below 2^31
+ * A block's scale is the smallest k with max |x| <= 448 * 2^k over its finite
+ * values (k of -126 .. 127), the codes are x * 2^-k rounded to nearest even, so
+ * that no finite value saturates; NaN and infinities become a NaN code (there are two).
+ *
+ * st_mx8_load - the values back in fp32 or bf16 (both hold them exactly; what was
+ * rounded up to 2^128 comes back as infinity), through
+ * an activation if act is not ST_ACT_NONE: out = act(x).
+ * x and out must not overlap.
+ * Errors of both: ST_ERR_INVALID_ARG, ST_ERR_BAD_SHAPE, ST_ERR_ALIGNMENT, ST_ERR_HIP.
+ */
+st_status st_mx8_store(int64_t rows, int64_t channels, const st_rows* x, const st_rows* out, void* stream);
+st_status st_mx8_load(int64_t rows, int64_t channels, const st_rows* x, int32_t act, const st_rows* out, void* stream);
+
+/*
+ * st_rmsnorm - root-mean-square norm of x + residual over the channels of every row:
+ *   s = x + residual (or x), rounded to the type it is kept in
+ *   y = s * rstd * gamma_c,  rstd = 1 / sqrt(mean of s^2 over the channels + eps)
+ *   rows >= 0, channels 1 .. 16384
+ *   x, residual_or_null   fp32 or bf16, each its own
+ *   gamma_or_null         `channels` floats or NULL (1)
+ *   eps                   finite, >= 0
+ *   total_or_null         s, fp32 or bf16 (its type rounds s; without it s is fp32);
+ *                         may be x or residual themselves in their own type and stride
+ *   y_or_null             y in fp32 or bf16
+ *   y8_or_null            y in the 8-bit form, rounded from fp32 (either output or both)
+ *   rstd_or_null          one float per row: what the backward pass reads
+ * One pass over the rows; sums are fp32.
+ *
+ * st_rmsnorm_backward - gradients for dy at y and dtotal at s (what flows along
+ * the residual stream past the norm):
+ *   dx = dtotal + rstd * (g - xh * mean(g * xh)),  g = dy * gamma_c, xh = s * rstd
+ *   dgamma = sum over rows of dy * xh
+ *   s               the forward call's sum, in fp32, bf16 or the 8-bit form
+ *   dtotal_or_null  fp32 or bf16, or NULL (0)
+ *   dx              the gradient at x and at residual, fp32 or bf16; may be dy or
+ *                   dtotal themselves in their own type and stride
+ *   dgamma_or_null  `channels` floats
+ *   workspace       >= st_rmsnorm_backward_workspace_bytes(rows, channels) bytes
+ * dgamma is summed in fp32 in an order fixed by the sizes and types (no atomics).
+ * Errors of both: ST_ERR_INVALID_ARG, ST_ERR_BAD_SHAPE (outputs that overlap an
+ * input or one another), ST_ERR_UNSUPPORTED (more than 16384 channels, 2^31 rows),
+ * ST_ERR_WORKSPACE, ST_ERR_ALIGNMENT, ST_ERR_HIP.
+ */
+st_status st_rmsnorm(int64_t rows, int64_t channels, const st_rows* x, const st_rows* residual_or_null,
+                     const float* gamma_or_null, float eps, const st_rows* total_or_null, const st_rows* y_or_null,
+                     const st_rows* y8_or_null, float* rstd_or_null, void* stream);
+size_t st_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t channels);
+st_status st_rmsnorm_backward(int64_t rows, int64_t channels, const st_rows* s, const st_rows* dy,
+                              const st_rows* dtotal_or_null, const float* gamma_or_null, const float* rstd,
+                              const st_rows* dx, float* dgamma_or_null, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* --------------------------------------------------------- matrix products */
+
+/*
+ * st_linear - y = act(x w^T + bias) + residual in one pass over the products.
+ *   rows, in, out     x is [rows][in], w [out][in], y [rows][out]; rows >= 0, in and
+ *                     out >= 1, all below 2^31
+ *   x, w              one type: fp32, bf16, or both in the 8-bit form (inference)
+ *   bias_or_null      `out` floats
+ *   act               ST_ACT_*
+ *   residual_or_null  [rows][out], fp32 or bf16, added after the activation
+ *   y                 fp32, bf16 or the 8-bit form (rounded from fp32); may be residual
+ *                     itself in its own type and stride
+ *   pre_or_null       receives x w^T + bias, in any of the three types: what the
+ *                     gradient of the activation reads
+ *   workspace         >= st_linear_workspace_bytes(rows, in, out, type, 0) bytes
+ * bf16 operands multiply on the matrix cores with fp32 accumulation, fp32 operands
+ * in fp32.  8-bit operands do so too where y and pre are no fp32; with an fp32
+ * output they are widened to bf16 (exactly) on the way, since the 8-bit instructions
+ * cut the products of eight steps 13 bits below the largest.  Few rows stream the weights once; where tiles are few
+ * the products' sum is split over workgroups and joined in a fixed order: the
+ * bits depend on sizes and types only.
+ * Errors: ST_ERR_WORKSPACE, ST_ERR_ALIGNMENT, ST_ERR_BAD_SHAPE, ST_ERR_UNSUPPORTED (rows of
+ * 4 MiB or more), ST_ERR_INVALID_ARG, ST_ERR_HIP.
+ */
+size_t st_linear_workspace_bytes(int64_t rows, int64_t in, int64_t out, int32_t type, int32_t backward);
+st_status st_linear(int64_t rows, int64_t in, int64_t out, const st_rows* x, const st_rows* w, const float* bias_or_null,
+                    int32_t act, const st_rows* residual_or_null, const st_rows* y, const st_rows* pre_or_null,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * st_linear_backward - gradients of st_linear for dy at y:
+ *   p = dy * act'(pre);  dx = p w;  dw = p^T x;  dbias = sum of p over the rows
+ * (the gradient at residual is dy itself).
+ *   x               the forward call's input: w's type, or the 8-bit form it was
+ *                   kept in
+ *   w               fp32 or bf16; the products run in its type (p is rounded to it)
+ *   pre_or_null     as the forward call wrote it, any type; NULL with ST_ACT_NONE only
+ *   dy              fp32 or bf16
+ *   dx_or_null, dw_or_null   fp32 or bf16, or NULL (not computed); must not
+ *                   overlap an input
+ *   dbias_or_null   `out` floats (summed from fp32 p), or NULL
+ *   workspace       >= st_linear_workspace_bytes(rows, in, out, w's type, 1) bytes
+ * rows == 0 clears dw and dbias.  No atomics: the bits depend on sizes and types
+ * only.  Errors as st_linear.
+ */
+st_status st_linear_backward(int64_t rows, int64_t in, int64_t out, const st_rows* x, const st_rows* w, int32_t act,
+                             const st_rows* pre_or_null, const st_rows* dy, const st_rows* dx_or_null,
+                             const st_rows* dw_or_null, float* dbias_or_null, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
 #ifdef __cplusplus
 }
 #endif
