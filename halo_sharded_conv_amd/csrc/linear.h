@@ -39,17 +39,21 @@ template <int PITCH> __device__ __forceinline__ constexpr int chunk_swizzle(int 
   return PITCH == 64 ? (r >> 2) & 3 : PITCH == 128 ? (((r >> 1) & 1) << 2) | ((r >> 2) & 3) : ((r & 3) << 2) | ((r >> 2) & 3);
 }
 
-// One operand's tile of a stage: 64 bytes of the contraction for W rows of the
-// operand.  As it lies in memory: [W rows][64 bytes] where the contraction is
-// contiguous (COL false), [64 / size contraction rows][W] where the operand's own
-// rows are (COL true).  STEPS: fragments along a stage.
+// One operand's tile of a stage: 128 bytes of the contraction (a cache line) for W
+// rows of the operand.  As it lies in memory: [W rows][128 bytes] where the
+// contraction is contiguous (COL false), [128 / size contraction rows][W] where the
+// operand's own rows are (COL true).
 template <class T, bool COL, int W, int NW> struct Oper {
-  static constexpr int KT = 64 / T::kSize;              // contraction steps of a stage
-  static constexpr int PITCH = COL ? W * T::kSize : 64;
+  static constexpr int KT = 128 / T::kSize;             // contraction steps of a stage
+  static constexpr int PITCH = COL ? W * T::kSize : 128;
   static constexpr int CH = PITCH / 16;
-  static constexpr int BYTES = W * 64;
+  static constexpr int BYTES = W * 128;
   static constexpr int NI = BYTES / 1024 / NW;          // transfers of 1 KB per wave
   static_assert(BYTES % (1024 * NW) == 0, "whole transfers");
+  // a wave's next transfer: so many rows on, and with the same chunks where the
+  // permutation repeats by then
+  static constexpr int ROWS_ON = 64 * NW / CH;
+  static constexpr bool ALIKE = ROWS_ON % 16 == 0;
 
   static __device__ __forceinline__ int dma_row(int wave, int lane, int i) { return ((i * NW + wave) * 64 + lane) / CH; }
   static __device__ __forceinline__ int dma_byte(int wave, int lane, int i) {
@@ -62,11 +66,11 @@ template <class T, bool COL, int W, int NW> struct Oper {
   }
 };
 
-// Fragments and products by type.  STEPS fragments cover a stage's 64 bytes.
+// Fragments and products by type.  STEPS fragments cover a stage.
 template <class T> struct Prod;
 template <> struct Prod<BF16> {
   using Frag = bf16x8;                                  // 16 contraction steps, 8 a half
-  static constexpr int STEPS = 2;
+  static constexpr int STEPS = 4;
   template <bool COL, int W, int NW> static __device__ __forceinline__ Frag frag(const char* tile, int b, int s, int lane) {
     using O = Oper<BF16, COL, W, NW>;
     const int half = lane >> 5;
@@ -85,13 +89,13 @@ template <> struct Prod<BF16> {
       return __builtin_bit_cast(Frag, __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
-  static __device__ __forceinline__ f32x16 mul(const Frag& a, const Frag& b, f32x16 c, int, int) {
+  template <int S> static __device__ __forceinline__ f32x16 mul(const Frag& a, const Frag& b, f32x16 c, int, int) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
 };
 template <> struct Prod<F32> {
   using Frag = f32x4_t;                                 // 8 contraction steps, 4 a half, over four products
-  static constexpr int STEPS = 2;
+  static constexpr int STEPS = 4;
   template <bool COL, int W, int NW> static __device__ __forceinline__ Frag frag(const char* tile, int b, int s, int lane) {
     using O = Oper<F32, COL, W, NW>;
     const int l = lane & 31, half = lane >> 5;
@@ -105,7 +109,7 @@ template <> struct Prod<F32> {
       return v;
     }
   }
-  static __device__ __forceinline__ f32x16 mul(const Frag& a, const Frag& b, f32x16 c, int, int) {
+  template <int S> static __device__ __forceinline__ f32x16 mul(const Frag& a, const Frag& b, f32x16 c, int, int) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
     return c;
@@ -116,22 +120,22 @@ template <> struct Prod<MX8> {
   // block of 32 in a lane's first and second 16 bytes.  It takes the blocks' scales
   // from the lanes: block b's from half b.
   using Frag = i32x8;
-  static constexpr int STEPS = 1;
+  static constexpr int STEPS = 2;
   static __device__ __forceinline__ Frag join(u32x4_t lo, u32x4_t hi) {
     return Frag{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
   }
-  template <bool COL, int W, int NW> static __device__ __forceinline__ Frag frag(const char* tile, int b, int, int lane) {
+  template <bool COL, int W, int NW> static __device__ __forceinline__ Frag frag(const char* tile, int b, int s, int lane) {
     static_assert(!COL, "blocks run along the contraction");
     using O = Oper<MX8, false, W, NW>;
     const int r = 32 * b + (lane & 31), half = lane >> 5;
-    return join(*reinterpret_cast<const u32x4_t*>(O::at(tile, r, half)), *reinterpret_cast<const u32x4_t*>(O::at(tile, r, 2 + half)));
+    return join(*reinterpret_cast<const u32x4_t*>(O::at(tile, r, 4 * s + half)), *reinterpret_cast<const u32x4_t*>(O::at(tile, r, 4 * s + 2 + half)));
   }
-  // sa, sb: scale bytes of this lane's row and of block `half`, in the low bytes.
+  // sa, sb: scale bytes of this lane's row; block 2 S + half of the stage in byte 2 S.
   // Inside the instruction the products of eight steps are aligned to the largest of
   // them and cut 13 bits below its leading bit; beyond, the sums are fp32.  That is
   // below what an output in bf16 or 8 bits shows; fp32 outputs take Prod<MX8X>.
-  static __device__ __forceinline__ f32x16 mul(const Frag& a, const Frag& b, f32x16 c, int sa, int sb) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, sa, 0, sb);
+  template <int S> static __device__ __forceinline__ f32x16 mul(const Frag& a, const Frag& b, f32x16 c, int sa, int sb) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 2 * S, sa, 2 * S, sb);
   }
 };
 // 8-bit operands whose products are summed in fp32 throughout: every value is
@@ -140,13 +144,13 @@ template <> struct Prod<MX8> {
 struct MX8X { static constexpr int kSize = 1; };
 template <> struct Prod<MX8X> {
   struct Frag { bf16x8 v[4]; };
-  static constexpr int STEPS = 1;
-  template <bool COL, int W, int NW> static __device__ __forceinline__ i32x8 raw(const char* tile, int b, int lane) {
+  static constexpr int STEPS = 2;
+  template <bool COL, int W, int NW> static __device__ __forceinline__ i32x8 raw(const char* tile, int b, int s, int lane) {
     static_assert(!COL, "blocks run along the contraction");
     using O = Oper<MX8, false, W, NW>;
     const int r = 32 * b + (lane & 31), half = lane >> 5;
-    return Prod<MX8>::join(*reinterpret_cast<const u32x4_t*>(O::at(tile, r, 2 * half)),
-                           *reinterpret_cast<const u32x4_t*>(O::at(tile, r, 2 * half + 1)));
+    return Prod<MX8>::join(*reinterpret_cast<const u32x4_t*>(O::at(tile, r, 4 * s + 2 * half)),
+                           *reinterpret_cast<const u32x4_t*>(O::at(tile, r, 4 * s + 2 * half + 1)));
   }
   static __device__ __forceinline__ Frag widen(const i32x8& w, int scale) {
     Frag f;
@@ -160,7 +164,7 @@ template <> struct Prod<MX8X> {
     }
     return f;
   }
-  static __device__ __forceinline__ f32x16 mul(const Frag& a, const Frag& b, f32x16 c, int, int) {
+  template <int S> static __device__ __forceinline__ f32x16 mul(const Frag& a, const Frag& b, f32x16 c, int, int) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v[i], b.v[i], c, 0, 0, 0);
     return c;
@@ -185,29 +189,50 @@ __device__ __forceinline__ uint32_t swap_max(uint32_t v) {
 // to an output in its type.
 __device__ __forceinline__ void put_block(const Rows& o, int64_t m, int n0, int cols, int half, const float (&v)[16]) {
   if (o.type == ST_MX8) {
+    // (channels past the last are zeros here: they have no part in the scale)
     uint32_t top = 0;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) top = max(top, n0 + 8 * (r / 4) + 4 * half + r % 4 < cols ? mx_bits(v[r]) : 0u);
-    const int s = mx_scale(swap_max(top));
+    for (int r = 0; r < 16; ++r) top = max(top, mag_bits(v[r]));
+    top = swap_max(top);
+    uint32_t w[4];
+    int s;
+    if (__builtin_amdgcn_ballot_w64(top >= 0x7F800000u) == 0) {
+      s = mx_scale(top);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = n0 + 8 * q + 4 * half;
-      store_codes<4>(o, m, n, cols - n, {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]}, s);
+      for (int q = 0; q < 4; ++q) w[q] = mx_codes<false>(v + 4 * q, s);
+    } else {                                            // NaN or infinity in some block of the wave
+      top = 0;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = max(top, mx_bits(v[r]));
+      s = mx_scale(swap_max(top));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[q] = mx_codes<true>(v + 4 * q, s);
+    }
+    uint8_t* p = reinterpret_cast<uint8_t*>(o.p) + m * o.stride + n0;
+    if (half == 0) o.scales[m * o.scale_stride + (n0 >> 5)] = (uint8_t)s;
+    if (n0 + 32 <= cols) {
+      // the lanes of one token trade quads: 16 channels in a row each
+      const u32x2_t a = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false));
+      const u32x2_t b = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false));
+      *reinterpret_cast<u32x4_t*>(p + 16 * half) = u32x4_t{a[0], a[1], b[0], b[1]};
+    } else {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int n = 8 * (r / 4) + 4 * half + r % 4;
+        if (n0 + n < cols) p[n] = (uint8_t)(w[r / 4] >> (8 * (r % 4)));
+      }
     }
     return;
   }
   char* p = o.p + m * o.stride;
   if (o.type == ST_BF16 && n0 + 32 <= cols) {
-    // the lanes of one token trade quads, so that each stores 8 channels in a row
+    // the lanes of one token trade quads: 8 channels in a row each, twice
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      u32x2_t lo, hi;
-      {
-        const uint32_t a0 = pack_bf16(v[8 * j], v[8 * j + 1]), a1 = pack_bf16(v[8 * j + 2], v[8 * j + 3]);
-        const uint32_t b0 = pack_bf16(v[8 * j + 4], v[8 * j + 5]), b1 = pack_bf16(v[8 * j + 6], v[8 * j + 7]);
-        lo = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(a0, b0, false, false));
-        hi = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(a1, b1, false, false));
-      }
+      const uint32_t a0 = pack_bf16(v[8 * j], v[8 * j + 1]), a1 = pack_bf16(v[8 * j + 2], v[8 * j + 3]);
+      const uint32_t b0 = pack_bf16(v[8 * j + 4], v[8 * j + 5]), b1 = pack_bf16(v[8 * j + 6], v[8 * j + 7]);
+      const u32x2_t lo = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(a0, b0, false, false));
+      const u32x2_t hi = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(a1, b1, false, false));
       *reinterpret_cast<u32x4_any*>(p + (int64_t)(n0 + 16 * j + 8 * half) * 2) = u32x4_t{lo[0], hi[0], lo[1], hi[1]};
     }
     return;
@@ -219,34 +244,26 @@ __device__ __forceinline__ void put_block(const Rows& o, int64_t m, int n0, int 
   }
 }
 
-// pre = acc + bias; y = act(pre) + residual.  Both lanes of a token come here.
+// v = x w^T + bias: pre = v; y = act(v) + residual.  Both lanes of a token come here.
 __device__ __forceinline__ void finish_block(const Finish& f, int64_t m, int n0, int half, float (&v)[16]) {
   if (m >= f.rows || n0 >= f.cols) return;
-  if (f.bias) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = n0 + 8 * q + 4 * half;
-      float t[4];
-      load_some<F32, 4>(reinterpret_cast<const char*>(f.bias + n), f.cols - n, t);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * q + i] += t[i];
-    }
-  }
-  if (f.pre.type >= 0) put_block(f.pre, m, n0, f.cols, half, v);
-  if (f.act != kActNone) {
-#pragma unroll
-    for (int r = 0; r < 16; ++r) v[r] = act_of(f.act, v[r]);
-  }
-  if (f.res.type >= 0) {
+  float t[16];
+  if (f.res.type >= 0) {                                // (on its way during the activation)
     const char* p = f.res.p + m * f.res.stride;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int n = n0 + 8 * q + 4 * half;
-      float t[4];
-      load_some<4>(f.res.type, p + (int64_t)n * (f.res.type == ST_F32 ? 4 : 2), f.cols - n, t);
+      float u[4];
+      load_some<4>(f.res.type, p + (int64_t)n * (f.res.type == ST_F32 ? 4 : 2), f.cols - n, u);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * q + i] += t[i];
+      for (int i = 0; i < 4; ++i) t[4 * q + i] = u[i];
     }
+  }
+  if (f.pre.type >= 0) put_block(f.pre, m, n0, f.cols, half, v);
+  if (f.act != kActNone) activate(f.act, v);
+  if (f.res.type >= 0) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) v[r] += t[r];
   }
   put_block(f.y, m, n0, f.cols, half, v);
 }

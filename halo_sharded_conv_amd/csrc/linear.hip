@@ -14,6 +14,14 @@
 namespace st {
 namespace {
 
+template <int I> using Int = std::integral_constant<int, I>;
+template <int N, int I = 0, class F> __device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (I < N) {
+    f(Int<I>{});
+    static_for<N, I + 1>(f);
+  }
+}
+
 struct GemmArgs {
   Rows a, b;
   Finish f;
@@ -27,22 +35,23 @@ struct GemmArgs {
 
 template <class T, bool AC, bool BC, int TA, int TB, int WA, int WB, int OCC>
 __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
+#ifdef __HIP_DEVICE_COMPILE__                           // (the host pass needs the name alone)
   constexpr int NW = WA * WB, PA = TA / WA, PB = TB / WB, NA = PA / 32, NB = PB / 32;
   using P = Prod<T>;
   using OA = Oper<T, AC, TA, NW>;
   using OB = Oper<T, BC, TB, NW>;
-  constexpr int KT = OA::KT, NI = OA::NI + OB::NI;
+  constexpr int KT = OA::KT, STEPS = P::STEPS;
   constexpr bool EXACT = std::is_same<T, MX8X>::value, MX = std::is_same<T, MX8>::value || EXACT;
+  constexpr int SCALES = MX ? (TA + TB) * 16 : 16;      // 16 scale bytes of every row: four stages
   __shared__ __attribute__((aligned(1024))) char a0[OA::BYTES];
   __shared__ __attribute__((aligned(1024))) char a1[OA::BYTES];
-  __shared__ __attribute__((aligned(1024))) char a2[OA::BYTES];
   __shared__ __attribute__((aligned(1024))) char b0[OB::BYTES];
   __shared__ __attribute__((aligned(1024))) char b1[OB::BYTES];
-  __shared__ __attribute__((aligned(1024))) char b2[OB::BYTES];
+  __shared__ __attribute__((aligned(1024))) char sc[2 * SCALES];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, wa = wave % WA, wb = wave / WA;
 
-  // workgroups go round the 8 XCDs: each takes a run of tiles, eight row tiles
+  // workgroups go round the 8 XCDs: each takes a run of tiles, some row tiles
   // deep, so that what its L2 holds is shared
   int ta, tb, split;
   {
@@ -59,121 +68,181 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
   const int n0 = ta * TA, m0 = tb * TB;
   const int k_lo = split * g.per_split, k_hi = min(g.stages, k_lo + g.per_split);
 
-  // this lane's transfers: byte offsets from a stage's base
-  uint32_t offa[OA::NI], offb[OB::NI];
+  // this lane's transfers: byte offsets from a stage's base, of the first one where
+  // the others are rows on
+  constexpr int QA = OA::ALIKE ? 1 : OA::NI, QB = OB::ALIKE ? 1 : OB::NI;
+  uint32_t offa[QA], offb[QB];
 #pragma unroll
-  for (int i = 0; i < OA::NI; ++i) {
+  for (int i = 0; i < QA; ++i) {
     const int r = OA::dma_row(wave, lane, i), b = OA::dma_byte(wave, lane, i);
     offa[i] = AC && n0 * T::kSize + b >= g.n * T::kSize ? kPastEnd : (uint32_t)(r * (int)g.a.stride + b);
   }
 #pragma unroll
-  for (int i = 0; i < OB::NI; ++i) {
+  for (int i = 0; i < QB; ++i) {
     const int r = OB::dma_row(wave, lane, i), b = OB::dma_byte(wave, lane, i);
     offb[i] = BC && m0 * T::kSize + b >= g.m * T::kSize ? kPastEnd : (uint32_t)(r * (int)g.b.stride + b);
   }
   const char* pa = AC ? g.a.p + (int64_t)n0 * T::kSize : g.a.p + (int64_t)n0 * g.a.stride;
   const char* pb = BC ? g.b.p + (int64_t)m0 * T::kSize : g.b.p + (int64_t)m0 * g.b.stride;
-  // scale bytes of this lane's rows (8-bit operands)
-  uint32_t soa[MX ? NA : 1], sob[MX ? NB : 1];
-  int sa[MX ? NA : 1], sb[MX ? NB : 1];
-  if constexpr (MX) {
-#pragma unroll
-    for (int i = 0; i < NA; ++i) soa[i] = (uint32_t)((wa * PA + 32 * i + (lane & 31)) * (int)g.a.scale_stride + half);
-#pragma unroll
-    for (int i = 0; i < NB; ++i) sob[i] = (uint32_t)((wb * PB + 32 * i + (lane & 31)) * (int)g.b.scale_stride + half);
-  }
 
-  // Stage kt's transfers.  Past the last stage nothing is read: the transfers write
-  // zeros, so that every step waits for the same number of them.
+  // Stage kt's transfers.  Past the last stage nothing is read: they write zeros.
   const int sta = (int)g.a.stride, stb = (int)g.b.stride;
-  auto fetch = [&](char* as, char* bs, int kt) __attribute__((always_inline)) {
-    const int left = g.kbytes - kt * 64;                // bytes of the contraction from here on
+  auto fetch = [&](char* as, char* bs, int kt) __attribute__((always_inline)) -> void {
+    const int left = g.kbytes - kt * 128;               // bytes of the contraction from here on
     const int rows = min(g.k - kt * KT, KT);            // its steps of this stage
     const int na = AC ? rows * sta : min(TA, g.n - n0) * sta, nb = BC ? rows * stb : min(TB, g.m - m0) * stb;
     const auto ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(AC ? pa + (int64_t)kt * KT * sta : pa), (short)0,
                                                       kt < k_hi ? na : 0, 0x00020000);
     const auto rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(BC ? pb + (int64_t)kt * KT * stb : pb), (short)0,
                                                       kt < k_hi ? nb : 0, 0x00020000);
+    // (kPastEnd stays past every end with the rows added)
+    static_assert((AC || OA::ALIKE) && (BC || OB::ALIKE), "one byte offset for all transfers along the contraction");
+    const uint32_t a_first = !AC && OA::dma_byte(wave, lane, 0) >= left ? kPastEnd : offa[0];
+    const uint32_t b_first = !BC && OB::dma_byte(wave, lane, 0) >= left ? kPastEnd : offb[0];
 #pragma unroll
-    for (int i = 0; i < OA::NI; ++i) {
-      const uint32_t at = !AC && OA::dma_byte(wave, lane, i) >= left ? kPastEnd : offa[i];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void)OA::dma_dst(as, wave, i), 16, at, AC ? 0 : kt * 64, 0, 0);
-    }
+    for (int i = 0; i < OA::NI; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void)OA::dma_dst(as, wave, i), 16,
+                                               OA::ALIKE ? a_first + (uint32_t)(i * OA::ROWS_ON * sta) : offa[i % QA], AC ? 0 : kt * 128, 0, 0);
 #pragma unroll
-    for (int i = 0; i < OB::NI; ++i) {
-      const uint32_t at = !BC && OB::dma_byte(wave, lane, i) >= left ? kPastEnd : offb[i];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void)OB::dma_dst(bs, wave, i), 16, at, BC ? 0 : kt * 64, 0, 0);
-    }
+    for (int i = 0; i < OB::NI; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void)OB::dma_dst(bs, wave, i), 16,
+                                               OB::ALIKE ? b_first + (uint32_t)(i * OB::ROWS_ON * stb) : offb[i % QB], BC ? 0 : kt * 128, 0, 0);
   };
-  auto scales = [&](int kt) __attribute__((always_inline)) {
+  // 8-bit operands: the scale bytes of stages kt .. kt + 3, 16 of every row (a row's
+  // may end before; the bytes past it are not used)
+  auto fetch_scales = [&](int kt) __attribute__((always_inline)) -> void {
     if constexpr (MX) {
-      const auto ra = rows_rsrc(g.a.scales + (int64_t)n0 * g.a.scale_stride, (int64_t)min(TA, g.n - n0) * g.a.scale_stride);
-      const auto rb = rows_rsrc(g.b.scales + (int64_t)m0 * g.b.scale_stride, (int64_t)min(TB, g.m - m0) * g.b.scale_stride);
-      // (past the last block the codes are zero; a scale byte there may be NaN's)
-      const uint32_t none = 2 * kt + half >= g.blocks_k ? kPastEnd : 0u;
-#pragma unroll
-      for (int i = 0; i < NA; ++i) sa[i] = __builtin_amdgcn_raw_buffer_load_b8(ra, none | soa[i], 2 * kt, 0);
-#pragma unroll
-      for (int i = 0; i < NB; ++i) sb[i] = __builtin_amdgcn_raw_buffer_load_b8(rb, none | sob[i], 2 * kt, 0);
+      if (wave < (TA + TB) / 64) {
+        const bool of_a = wave < TA / 64;
+        const Rows& o = of_a ? g.a : g.b;
+        const int row0 = of_a ? n0 : m0, rows = of_a ? min(TA, g.n - n0) : min(TB, g.m - m0), first = of_a ? wave * 64 : wave * 64 - TA;
+        const auto rs = __builtin_amdgcn_make_buffer_rsrc(o.scales + (int64_t)row0 * o.scale_stride, (short)0,
+                                                          kt < k_hi ? rows * (int)o.scale_stride : 0, 0x00020000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void)(sc + ((kt - k_lo) >> 2 & 1) * SCALES + wave * 1024), 16,
+                                                 (uint32_t)((first + lane) * (int)o.scale_stride), kt * 4, 0, 0);
+      }
     }
   };
 
+  // the sums start from the bias (the first split's do; zeros past the last channel)
   f32x16 acc[NA][NB];
+  {
+    const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(g.f.bias), (short)0, g.f.bias && split == 0 ? g.n * 4 : 0, 0x00020000);
 #pragma unroll
-  for (int i = 0; i < NA; ++i)
+    for (int i = 0; i < NA; ++i) {
 #pragma unroll
-    for (int j = 0; j < NB; ++j) acc[i][j] = f32x16{};
-
-  // Stage kt in (as, bs); stage kt + 2 goes to (an, bn), which every wave has
-  // finished reading once it is past the barrier.  The NI transfers of stage kt + 1
-  // may still be under way behind the barrier.
-  auto step = [&](const char* as, const char* bs, char* an, char* bn, int kt) __attribute__((always_inline)) {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070 | (NI & 15) | (NI >> 4) << 14);
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    int ca[MX ? NA : 1], cb[MX ? NB : 1];
-    if constexpr (MX) {
+      for (int q = 0; q < 4; ++q) {
+        const f32x4_t t = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (n0 + wa * PA + 32 * i + 8 * q + 4 * half) * 4, 0, 0));
 #pragma unroll
-      for (int i = 0; i < NA; ++i) ca[i] = sa[i];
+        for (int e = 0; e < 4; ++e) acc[i][0][4 * q + e] = t[e];
+      }
 #pragma unroll
-      for (int i = 0; i < NB; ++i) cb[i] = sb[i];
-      scales(kt + 1);
-      asm volatile("" ::: "memory");                    // (ahead of the transfers: the next step's wait covers them)
+      for (int j = 1; j < NB; ++j) acc[i][j] = acc[i][0];
     }
-    fetch(an, bn, kt + 2);
-#pragma unroll
-    for (int s = 0; s < P::STEPS; ++s) {
-      typename P::Frag fa[NA], fb[NB];
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        if constexpr (EXACT) fb[j] = P::widen(P::template raw<BC, TB, NW>(bs, wb * NB + j, lane), cb[j]);
-        else fb[j] = P::template frag<BC, TB, NW>(bs, wb * NB + j, s, lane);
-      }
-#pragma unroll
-      for (int i = 0; i < NA; ++i) {
-        if constexpr (EXACT) fa[i] = P::widen(P::template raw<AC, TA, NW>(as, wa * NA + i, lane), ca[i]);
-        else fa[i] = P::template frag<AC, TA, NW>(as, wa * NA + i, s, lane);
-      }
+  }
+
+  typename P::Frag fa[2][NA], fb[2][NB];
+  int sa[2][MX ? NA : 1], sb[2][MX ? NB : 1];           // scale bytes of a stage: block 2 s + half in byte 2 s
+  auto read_scales = [&](auto SET, int kt) __attribute__((always_inline)) -> void {
+    if constexpr (MX) {
+      constexpr int set = decltype(SET)::value;
+      const char* p = sc + ((kt - k_lo) >> 2 & 1) * SCALES + ((kt - k_lo) & 3) * 4;
+      // (past the last block the codes are zero; a byte there may be NaN's)
+      const int blocks = g.blocks_k - 4 * kt;
+      const uint32_t mask = blocks >= 4 ? 0xFFFFFFFFu : blocks <= 0 ? 0u : (1u << 8 * blocks) - 1;
 #pragma unroll
       for (int i = 0; i < NA; ++i)
+        sa[set][i] = (int)((*reinterpret_cast<const uint32_t*>(p + (wa * PA + 32 * i + (lane & 31)) * 16) & mask) >> 8 * half);
 #pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = P::mul(fa[i], fb[j], acc[i][j], MX ? ca[MX ? i : 0] : 0, MX ? cb[MX ? j : 0] : 0);
+      for (int i = 0; i < NB; ++i)
+        sb[set][i] = (int)((*reinterpret_cast<const uint32_t*>(p + (TA + wb * PB + 32 * i + (lane & 31)) * 16) & mask) >> 8 * half);
     }
   };
+  auto read = [&](auto SET, auto STEP, auto SCSET, const char* as, const char* bs) __attribute__((always_inline)) -> void {
+    constexpr int set = decltype(SET)::value, s = decltype(STEP)::value, c = decltype(SCSET)::value;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      if constexpr (EXACT) fb[set][j] = P::widen(P::template raw<BC, TB, NW>(bs, wb * NB + j, s, lane), sb[c][j] >> 16 * s & 255);
+      else fb[set][j] = P::template frag<BC, TB, NW>(bs, wb * NB + j, s, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      if constexpr (EXACT) fa[set][i] = P::widen(P::template raw<AC, TA, NW>(as, wa * NA + i, s, lane), sa[c][i] >> 16 * s & 255);
+      else fa[set][i] = P::template frag<AC, TA, NW>(as, wa * NA + i, s, lane);
+    }
+  };
+  auto multiply = [&](auto SET, auto STEP, auto SCSET) __attribute__((always_inline)) -> void {
+    constexpr int set = decltype(SET)::value, s = decltype(STEP)::value, c = decltype(SCSET)::value;
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        acc[i][j] = P::template mul<s>(fa[set][i], fb[set][j], acc[i][j], MX ? sa[c][MX ? i : 0] : 0, MX ? sb[c][MX ? j : 0] : 0);
+  };
+  // The order of a step: a product, then the reads of one of the next step's
+  // fragments: b's first, a's as soon as the one in its place has had its last
+  // product (so that they share registers); a transfer behind every product.
+  auto order = [&](auto MORE) __attribute__((always_inline)) -> void {
+    if constexpr (!EXACT && T::kSize < 4) {
+      constexpr int RA = MX || AC ? 2 : 1, RB = MX || BC ? 2 : 1;      // LDS reads of a fragment
+      static_for<NA * NB>([&](auto S) __attribute__((always_inline)) -> void {
+        constexpr int t = decltype(S)::value, last = NA * NB - 1;
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);             // a product
+        if constexpr (t < NB) __builtin_amdgcn_sched_group_barrier(0x100, RB, 0);
+        static_for<NA>([&](auto I) __attribute__((always_inline)) -> void {
+          constexpr int at = (decltype(I)::value + 1) * NB;
+          if constexpr (t == (at < last ? at : last)) __builtin_amdgcn_sched_group_barrier(0x100, RA, 0);
+        });
+        __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);             // a transfer
+        if constexpr (t == last / 2 && decltype(MORE)::value > 0) __builtin_amdgcn_sched_group_barrier(0x100, decltype(MORE)::value, 0);   // scale bytes
+      });
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Stage kt in (as, bs), stage kt + 1 on its way to (an, bn).  Fragments are read one
+  // step ahead of the products; before the last step's products every wave has read
+  // all of stage kt, so the workgroup meets there, stage kt + 2 sets out into the
+  // buffers of stage kt, and the first fragments of stage kt + 1 are on their way
+  // while the matrix cores still have a step to do.
+  auto stage = [&](auto CUR, char* as, char* bs, const char* an, const char* bn, int kt) __attribute__((always_inline)) -> void {
+    constexpr int cur = decltype(CUR)::value;
+    // (its buffer's last readers are two meetings back, its first three ahead)
+    if constexpr (MX && cur == 0) {
+      if ((kt - k_lo & 3) == 0) fetch_scales(kt + 4);
+    }
+    static_for<STEPS>([&](auto S) __attribute__((always_inline)) -> void {
+      constexpr int s = decltype(S)::value;
+      if constexpr (s == 0) read_scales(Int<1 - cur>{}, kt + 1);
+      if constexpr (s + 1 < STEPS) {
+        read(Int<(s + 1) & 1>{}, Int<s + 1>{}, Int<cur>{}, as, bs);
+      } else {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x0070);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        read(Int<0>{}, Int<0>{}, Int<1 - cur>{}, an, bn);
+        fetch(as, bs, kt + 2);
+      }
+      multiply(Int<s & 1>{}, Int<s>{}, Int<cur>{});
+      order(Int<MX && s == 0 ? NA + NB : 0>{});
+    });
+  };
 
-  scales(k_lo);
+  fetch_scales(k_lo);
   fetch(a0, b0, k_lo);
-  asm volatile("" ::: "memory");                        // (the first step's wait counts on this order)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
   fetch(a1, b1, k_lo + 1);
+  read_scales(Int<0>{}, k_lo);
+  read(Int<0>{}, Int<0>{}, Int<0>{}, a0, b0);
   int kt = k_lo;
-  for (; kt + 3 <= k_hi; kt += 3) {
-    step(a0, b0, a2, b2, kt);
-    step(a1, b1, a0, b0, kt + 1);
-    step(a2, b2, a1, b1, kt + 2);
+  for (; kt + 2 <= k_hi; kt += 2) {
+    stage(Int<0>{}, a0, b0, a1, b1, kt);
+    stage(Int<1>{}, a1, b1, a0, b0, kt + 1);
   }
-  if (kt < k_hi) step(a0, b0, a2, b2, kt);
-  if (kt + 1 < k_hi) step(a1, b1, a0, b0, kt + 1);
+  if (kt < k_hi) stage(Int<0>{}, a0, b0, a1, b1, kt);
   __builtin_amdgcn_s_waitcnt(0x0070);                   // (no transfer outlives the workgroup's LDS)
 
 #pragma unroll 1
@@ -198,6 +267,7 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
         *reinterpret_cast<f32x4_t*>(p + 8 * q) = f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
     }
   }
+#endif
 }
 
 // Adds the splits' partial sums in order and finishes the blocks, one a wave
@@ -230,7 +300,7 @@ struct Shape {                        // tile and what a compute unit holds of i
 };
 // large and small tile; fp32 (products a ninth as fast, twice the registers per
 // fragment) stays with 128 x 128
-constexpr Shape kShapes[2][2] = {{{256, 128, 2}, {128, 64, 4}}, {{128, 128, 2}, {128, 64, 4}}};
+constexpr Shape kShapes[2][2] = {{{256, 256, 1}, {128, 64, 3}}, {{128, 128, 2}, {128, 64, 3}}};
 inline const Shape& shape_of(int type, int s) { return kShapes[type == ST_F32][s]; }
 constexpr int kCus = 256;
 
@@ -243,7 +313,7 @@ struct Choice {
 // as much as some stages) plus the partial sums' way through memory.
 // exact: 8-bit operands with an fp32 output, which the small tile alone has.
 Choice choose(int64_t m, int64_t n, int64_t k, int type, bool exact) {
-  const int kt = type == ST_F32 ? 16 : type == ST_BF16 ? 32 : 64;
+  const int kt = 128 / type_size(type);
   const int64_t stages = (k + kt - 1) / kt;
   Choice best{};
   double least = INFINITY;
@@ -251,10 +321,11 @@ Choice choose(int64_t m, int64_t n, int64_t k, int type, bool exact) {
     const Shape& h = shape_of(type, s);
     const int64_t tiles = (n + h.ta - 1) / h.ta * ((m + h.tb - 1) / h.tb);
     // microseconds of one stage of a full compute unit
-    const double stage = (type == ST_F32 ? 4.0 : 1.0) * h.ta * h.tb * h.per_cu / 65536.0 * (s ? 0.65 : 0.55);
+    const double stage = (type == ST_F32 ? 4.0 : 1.0) * h.ta * h.tb * h.per_cu / 65536.0 * (s ? 1.3 : 0.9);
     for (int64_t splits = 1; splits <= 64; splits = splits < 4 ? splits + 1 : splits * 5 / 4) {
-      const int64_t per = (stages + splits - 1) / splits, real = (stages + per - 1) / per;
-      if (splits > 1 && (real != splits || per < 4)) continue;
+      int64_t per = (stages + splits - 1) / splits;
+      if (type == ST_MX8) per = (per + 3) / 4 * 4;       // (scale bytes come for four stages)
+      if (splits > 1 && ((stages + per - 1) / per != splits || per < 2)) continue;
       const double rounds = std::ceil((double)tiles * splits / (kCus * h.per_cu));
       const double fill = std::min(1.0, (double)tiles * splits / (kCus * h.per_cu));
       double t = rounds * (per * stage * std::max(fill, 1.0 / h.per_cu) + 2.0);
@@ -269,8 +340,8 @@ int64_t part_ld(int64_t n) { return (n + 31) / 32 * 32; }
 template <class T, bool AC, bool BC> st_status gemm_launch(const GemmArgs& g, int shape, hipStream_t st) {
   const unsigned grid = (unsigned)((int64_t)g.tiles_a * g.tiles_b * g.splits);
   if (shape == 0 && std::is_same<T, F32>::value) gemm<F32, AC, BC, 128, 128, 2, 2, 2><<<grid, 256, 0, st>>>(g);
-  else if (shape == 0) gemm<typename std::conditional<std::is_same<T, F32>::value, BF16, T>::type, AC, BC, 256, 128, 2, 2, 2><<<grid, 256, 0, st>>>(g);
-  else gemm<T, AC, BC, 128, 64, 2, 2, 4><<<grid, 256, 0, st>>>(g);
+  else if (shape == 0) gemm<typename std::conditional<std::is_same<T, F32>::value, BF16, T>::type, AC, BC, 256, 256, 2, 4, 2><<<grid, 512, 0, st>>>(g);
+  else gemm<T, AC, BC, 128, 64, 2, 2, std::is_same<T, MX8>::value ? 2 : 3><<<grid, 256, 0, st>>>(g);
   return launch_check("gemm");
 }
 
@@ -297,7 +368,7 @@ st_status product_launch(const Product& p, void* workspace, hipStream_t st) {
   const bool exact = p.type == ST_MX8 && (p.f.y.type == ST_F32 || p.f.pre.type == ST_F32);
   const Choice c = choose(p.m, p.n, p.k, p.type, exact);
   const Shape& h = shape_of(p.type, c.shape);
-  const int es = type_size(p.type), kt = 64 / es;
+  const int es = type_size(p.type), kt = 128 / es;
   GemmArgs g{};
   g.a = p.a;
   g.b = p.b;

@@ -106,11 +106,13 @@ template <bool ACT> __global__ __launch_bounds__(kGradThreads) void grad_pass(co
 #pragma unroll
     for (int u = 0; u < kGradUnroll; ++u) {
       const int64_t r = r0 + u * step;
+      if constexpr (ACT) {
+        slopes(a.act, z[u]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (ACT) g[u][i] = i < n ? g[u][i] * slope_of(a.act, z[u][i]) : 0.f;
-        sum[i] += g[u][i];
+        for (int i = 0; i < 8; ++i) g[u][i] = i < n ? g[u][i] * z[u][i] : 0.f;
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += g[u][i];
       if (a.p.type >= 0 && r < a.rows) {
         const int k = a.p_cols - c;                     // (the padding past the columns gets zeros)
         if (k > 0) store_some<8>(a.p.type, a.p.p + r * a.p.stride + (int64_t)c * (a.p.type == ST_F32 ? 4 : 2), k, g[u]);

@@ -70,10 +70,7 @@ template <bool ACT> __global__ __launch_bounds__(kMxThreads) void mx8_load(const
     float v[8];
     mx_values(w[i][0], s[i], v);
     mx_values(w[i][1], s[i], v + 4);
-    if constexpr (ACT) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = act_of(a.act, v[j]);
-    }
+    if constexpr (ACT) activate(a.act, v);
     if (g.n > 0) store_some<8>(a.out.type, a.out.p + (int64_t)g.row * a.out.stride + (int64_t)g.c * (a.out.type == ST_F32 ? 4 : 2), g.n, v);
   }
 }

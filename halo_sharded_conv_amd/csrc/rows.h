@@ -157,10 +157,11 @@ template <int VEC, bool NT = false> __device__ __forceinline__ void store_some(i
 
 // ---- the 8-bit form: e4m3 codes, one power of two per 32 channels
 
-// A value's magnitude bits as they count for its block's scale: those of a NaN or
-// an infinity do not (their codes are NaN codes at any scale)
+// Magnitude bits: those of a NaN or an infinity are 0x7F800000 or more, and do not
+// count for their block's scale (their codes are NaN codes at any scale)
+__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 __device__ __forceinline__ uint32_t mx_bits(float v) {
-  const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
+  const uint32_t b = mag_bits(v);
   return b < 0x7F800000u ? b : 0u;
 }
 // Scale byte (k + 127) of a block whose largest magnitude has these bits: the
@@ -172,14 +173,15 @@ __device__ __forceinline__ int mx_scale(uint32_t amax_bits) {
   return min(max(k, 1), 254);
 }
 __device__ __forceinline__ float pow2_of(int byte) { return __uint_as_float((uint32_t)byte << 23); }
-// four values as codes of scale byte s: v * 2^-k (exact) rounded to nearest even
-__device__ __forceinline__ uint32_t mx_codes(const float* v, int s) {
+// four values as codes of scale byte s: v * 2^-k (exact) rounded to nearest even.
+// A NaN gives a NaN code by itself, an infinity where SPECIAL.
+template <bool SPECIAL> __device__ __forceinline__ uint32_t mx_codes(const float* v, int s) {
   const float f = pow2_of(254 - s);
   float u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     u[i] = v[i] * f;
-    u[i] = fabsf(u[i]) <= 448.f ? u[i] : __builtin_nanf("");
+    if constexpr (SPECIAL) u[i] = fabsf(u[i]) <= 448.f ? u[i] : __builtin_nanf("");
   }
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(u[0], u[1], 0, false);
   w = __builtin_amdgcn_cvt_pk_fp8_f32(u[2], u[3], w, true);
@@ -209,7 +211,7 @@ template <int VEC> __device__ __forceinline__ void store_codes(const Rows& o, in
   uint8_t* p = reinterpret_cast<uint8_t*>(o.p) + row * o.stride + c;
   uint32_t w[VEC / 4];
 #pragma unroll
-  for (int i = 0; i < VEC / 4; ++i) w[i] = mx_codes(v + 4 * i, s);
+  for (int i = 0; i < VEC / 4; ++i) w[i] = mx_codes<true>(v + 4 * i, s);
   if (n >= VEC) {
     if constexpr (VEC == 8) *reinterpret_cast<u32x2_t*>(p) = u32x2_t{w[0], w[1]};
     else *reinterpret_cast<uint32_t*>(p) = w[0];
@@ -273,33 +275,56 @@ __device__ __forceinline__ float tail_poly(float a) {
 }
 constexpr float kHalfLog2e = 0.72134752044448170f, kLog2E = 1.4426950408889634f, kInvSqrt2Pi = 0.39894228040143268f;
 
-__device__ __forceinline__ float act_of(int act, float z) {
-  if (act == kActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
-  if (act == kActGelu) {
+// Infinities take the limits (exp2's argument and the clamped factor see to it), NaN
+// stays NaN through exp2.
+template <int ACT> __device__ __forceinline__ float act_of(float z) {
+  if constexpr (ACT == kActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
+  if constexpr (ACT == kActGelu) {
     // z Phi(z) = max(z, 0) - |z| Q(|z|)
-    const float a = fabsf(z), h = a * tail_poly(a) * exp2_fast(-kHalfLog2e * z * z);
-    return a < 13.f ? fmaxf(z, 0.f) - h : (z > 0.f ? z : (z != z ? z : 0.f));
+    const float a = fminf(fabsf(z), 13.f);
+    return fmaf(-a * tail_poly(a), exp2_fast(-kHalfLog2e * z * z), fmaxf(z, 0.f));
   }
-  if (act == kActSilu) {
-    const float s = z * rcp_fast(1.f + exp2_fast(-kLog2E * z));
-    return z > -80.f ? s : (z != z ? z : 0.f);
-  }
+  if constexpr (ACT == kActSilu) return fmaxf(z, -200.f) * rcp_fast(1.f + exp2_fast(-kLog2E * z));
   return z;
 }
 // derivative of the activation
-__device__ __forceinline__ float slope_of(int act, float z) {
-  if (act == kActRelu) return z > 0.f ? 1.f : 0.f;
-  if (act == kActGelu) {
+template <int ACT> __device__ __forceinline__ float slope_of(float z) {
+  if constexpr (ACT == kActRelu) return z > 0.f ? 1.f : 0.f;
+  if constexpr (ACT == kActGelu) {
     // Phi(z) + z phi(z)
-    const float a = fabsf(z), e = exp2_fast(-kHalfLog2e * z * z), q = tail_poly(a) * e;
-    const float s = (z > 0.f ? 1.f - q : q) + z * e * kInvSqrt2Pi;
-    return a < 13.f ? s : (z > 0.f ? 1.f : (z != z ? z : 0.f));
+    const float a = fminf(fabsf(z), 13.f), e = exp2_fast(-kHalfLog2e * z * z), q = tail_poly(a) * e;
+    return fmaf(fminf(fmaxf(z, -13.f), 13.f), e * kInvSqrt2Pi, z > 0.f ? 1.f - q : q);
   }
-  if (act == kActSilu) {
-    const float s = rcp_fast(1.f + exp2_fast(-kLog2E * z)), d = s * fmaf(z, 1.f - s, 1.f);
-    return z > -80.f ? (z < 80.f ? d : 1.f) : (z != z ? z : 0.f);
+  if constexpr (ACT == kActSilu) {
+    const float s = rcp_fast(1.f + exp2_fast(-kLog2E * z)), c = fminf(fmaxf(z, -200.f), 200.f);
+    return s * fmaf(c, 1.f - s, 1.f);
   }
   return 1.f;
+}
+// one branch for N values
+template <int N> __device__ __forceinline__ void activate(int act, float (&v)[N]) {
+  if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = act_of<kActGelu>(v[i]);
+  } else if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = act_of<kActSilu>(v[i]);
+  } else if (act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = act_of<kActRelu>(v[i]);
+  }
+}
+template <int N> __device__ __forceinline__ void slopes(int act, float (&v)[N]) {
+  if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = slope_of<kActGelu>(v[i]);
+  } else if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = slope_of<kActSilu>(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = slope_of<kActRelu>(v[i]);
+  }
 }
 
 // Launches that other operators make (mx8.hip)
