@@ -186,7 +186,38 @@ __device__ __forceinline__ uint32_t swap_max(uint32_t v) {
 }
 
 // One token's 32 channels (16 in this lane, the others in the lane half across)
-// to an output in its type.
+// to an output in bf16 or fp32.
+__device__ __forceinline__ void put_float(const Rows& o, int64_t m, int n0, int cols, int half, const float (&v)[16]) {
+  char* p = o.p + m * o.stride;
+  if (n0 + 32 <= cols) {
+    if (o.type == ST_BF16) {
+      // the lanes of one token trade quads: 8 channels in a row each, twice
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t a0 = pack_bf16(v[8 * j], v[8 * j + 1]), a1 = pack_bf16(v[8 * j + 2], v[8 * j + 3]);
+        const uint32_t b0 = pack_bf16(v[8 * j + 4], v[8 * j + 5]), b1 = pack_bf16(v[8 * j + 6], v[8 * j + 7]);
+        const u32x2_t lo = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(a0, b0, false, false));
+        const u32x2_t hi = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(a1, b1, false, false));
+        *reinterpret_cast<u32x4_any*>(p + (int64_t)(n0 + 16 * j + 8 * half) * 2) = u32x4_t{lo[0], hi[0], lo[1], hi[1]};
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4_any*>(p + (int64_t)(n0 + 8 * q + 4 * half) * 4) = f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    }
+    return;
+  }
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {                        // the last channels
+    const int n = n0 + 8 * (r / 4) + 4 * half + r % 4;
+    if (n < cols) {
+      if (o.type == ST_F32) reinterpret_cast<float*>(p)[n] = v[r];
+      else reinterpret_cast<uint16_t*>(p)[n] = (uint16_t)pack_bf16(v[r], 0.f);
+    }
+  }
+}
+
+// The same to an output in any type
 __device__ __forceinline__ void put_block(const Rows& o, int64_t m, int n0, int cols, int half, const float (&v)[16]) {
   if (o.type == ST_MX8) {
     // (channels past the last are zeros here: they have no part in the scale)
@@ -224,29 +255,17 @@ __device__ __forceinline__ void put_block(const Rows& o, int64_t m, int n0, int 
     }
     return;
   }
-  char* p = o.p + m * o.stride;
-  if (o.type == ST_BF16 && n0 + 32 <= cols) {
-    // the lanes of one token trade quads: 8 channels in a row each, twice
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t a0 = pack_bf16(v[8 * j], v[8 * j + 1]), a1 = pack_bf16(v[8 * j + 2], v[8 * j + 3]);
-      const uint32_t b0 = pack_bf16(v[8 * j + 4], v[8 * j + 5]), b1 = pack_bf16(v[8 * j + 6], v[8 * j + 7]);
-      const u32x2_t lo = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(a0, b0, false, false));
-      const u32x2_t hi = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(a1, b1, false, false));
-      *reinterpret_cast<u32x4_any*>(p + (int64_t)(n0 + 16 * j + 8 * half) * 2) = u32x4_t{lo[0], hi[0], lo[1], hi[1]};
-    }
-    return;
-  }
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int n = n0 + 8 * q + 4 * half;
-    if (n < cols) store_some<4>(o.type, p + (int64_t)n * (o.type == ST_F32 ? 4 : 2), cols - n, {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]});
-  }
+  put_float(o, m, n0, cols, half, v);
 }
 
 // v = x w^T + bias: pre = v; y = act(v) + residual.  Both lanes of a token come here.
-__device__ __forceinline__ void finish_block(const Finish& f, int64_t m, int n0, int half, float (&v)[16]) {
+// PLAIN: v alone, to bf16 or fp32.
+template <bool PLAIN> __device__ __forceinline__ void finish_block(const Finish& f, int64_t m, int n0, int half, float (&v)[16]) {
   if (m >= f.rows || n0 >= f.cols) return;
+  if constexpr (PLAIN) {
+    put_float(f.y, m, n0, f.cols, half, v);
+    return;
+  }
   float t[16];
   if (f.res.type >= 0) {                                // (on its way during the activation)
     const char* p = f.res.p + m * f.res.stride;

@@ -33,7 +33,9 @@ struct GemmArgs {
   int32_t blocks_k;                   // 8-bit: scale blocks along k
 };
 
-template <class T, bool AC, bool BC, int TA, int TB, int WA, int WB, int OCC>
+// PLAIN: partial sums, or an output in bf16 or fp32 with nothing but a bias; the
+// epilogue is laid out for every block, so that it is worth keeping short.
+template <class T, bool AC, bool BC, int TA, int TB, int WA, int WB, int OCC, bool PLAIN>
 __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
 #ifdef __HIP_DEVICE_COMPILE__                           // (the host pass needs the name alone)
   constexpr int NW = WA * WB, PA = TA / WA, PB = TB / WB, NA = PA / 32, NB = PB / 32;
@@ -51,39 +53,41 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, wa = wave % WA, wb = wave / WA;
 
-  // workgroups go round the 8 XCDs: each takes a run of tiles, some row tiles
-  // deep, so that what its L2 holds is shared
-  int ta, tb, split;
-  {
-    const uint32_t total = gridDim.x, id = blockIdx.x, x = id & 7, per = total >> 3, more = total & 7;
-    uint32_t t = x * per + min(x, more) + (id >> 3);
-    const uint32_t tiles = (uint32_t)g.tiles_a * g.tiles_b;
-    split = t / tiles;
-    t -= split * tiles;
-    const uint32_t deep = 8, group = deep * g.tiles_a, gi = t / group, first = gi * deep;
-    const uint32_t in = t - gi * group, d = min(deep, g.tiles_b - first);
-    tb = first + in % d;
-    ta = in / d;
-  }
-  const int n0 = ta * TA, m0 = tb * TB;
-  const int k_lo = split * g.per_split, k_hi = min(g.stages, k_lo + g.per_split);
-
+  // Workgroups go round the 8 XCDs: each XCD takes a run of tiles, eight row tiles
+  // deep, so that what its L2 holds is shared; a workgroup takes every so many-th of
+  // its XCD's run.
+  const uint32_t xcd = blockIdx.x & 7, tiles = (uint32_t)g.tiles_a * g.tiles_b, total = tiles * g.splits;
+  const uint32_t t_step = (gridDim.x + 7 - xcd) >> 3, t_end = (xcd + 1) * (total >> 3) + min(xcd + 1, total & 7);
+  uint32_t t = xcd * (total >> 3) + min(xcd, total & 7) + (blockIdx.x >> 3);
+  int n0, m0, split, k_lo, k_hi;
   // this lane's transfers: byte offsets from a stage's base, of the first one where
   // the others are rows on
   constexpr int QA = OA::ALIKE ? 1 : OA::NI, QB = OB::ALIKE ? 1 : OB::NI;
   uint32_t offa[QA], offb[QB];
+  const char *pa, *pb;
+  auto place = [&]() __attribute__((always_inline)) -> void {
+    int l = lane;
+    asm("" : "+v"(l));                                  // (formed anew for each tile: no registers held meanwhile)
+    split = t / tiles;
+    const uint32_t u = t - split * tiles, deep = 8, group = deep * g.tiles_a, gi = u / group, first = gi * deep;
+    const uint32_t in = u - gi * group, d = min(deep, g.tiles_b - first);
+    m0 = (first + in % d) * TB;
+    n0 = in / d * TA;
+    k_lo = split * g.per_split;
+    k_hi = min(g.stages, k_lo + g.per_split);
 #pragma unroll
-  for (int i = 0; i < QA; ++i) {
-    const int r = OA::dma_row(wave, lane, i), b = OA::dma_byte(wave, lane, i);
-    offa[i] = AC && n0 * T::kSize + b >= g.n * T::kSize ? kPastEnd : (uint32_t)(r * (int)g.a.stride + b);
-  }
+    for (int i = 0; i < QA; ++i) {
+      const int r = OA::dma_row(wave, l, i), b = OA::dma_byte(wave, l, i);
+      offa[i] = AC && n0 * T::kSize + b >= g.n * T::kSize ? kPastEnd : (uint32_t)(r * (int)g.a.stride + b);
+    }
 #pragma unroll
-  for (int i = 0; i < QB; ++i) {
-    const int r = OB::dma_row(wave, lane, i), b = OB::dma_byte(wave, lane, i);
-    offb[i] = BC && m0 * T::kSize + b >= g.m * T::kSize ? kPastEnd : (uint32_t)(r * (int)g.b.stride + b);
-  }
-  const char* pa = AC ? g.a.p + (int64_t)n0 * T::kSize : g.a.p + (int64_t)n0 * g.a.stride;
-  const char* pb = BC ? g.b.p + (int64_t)m0 * T::kSize : g.b.p + (int64_t)m0 * g.b.stride;
+    for (int i = 0; i < QB; ++i) {
+      const int r = OB::dma_row(wave, l, i), b = OB::dma_byte(wave, l, i);
+      offb[i] = BC && m0 * T::kSize + b >= g.m * T::kSize ? kPastEnd : (uint32_t)(r * (int)g.b.stride + b);
+    }
+    pa = AC ? g.a.p + (int64_t)n0 * T::kSize : g.a.p + (int64_t)n0 * g.a.stride;
+    pb = BC ? g.b.p + (int64_t)m0 * T::kSize : g.b.p + (int64_t)m0 * g.b.stride;
+  };
 
   // Stage kt's transfers.  Past the last stage nothing is read: they write zeros.
   const int sta = (int)g.a.stride, stb = (int)g.b.stride;
@@ -124,23 +128,7 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
     }
   };
 
-  // the sums start from the bias (the first split's do; zeros past the last channel)
   f32x16 acc[NA][NB];
-  {
-    const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(g.f.bias), (short)0, g.f.bias && split == 0 ? g.n * 4 : 0, 0x00020000);
-#pragma unroll
-    for (int i = 0; i < NA; ++i) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f32x4_t t = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (n0 + wa * PA + 32 * i + 8 * q + 4 * half) * 4, 0, 0));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][0][4 * q + e] = t[e];
-      }
-#pragma unroll
-      for (int j = 1; j < NB; ++j) acc[i][j] = acc[i][0];
-    }
-  }
-
   typename P::Frag fa[2][NA], fb[2][NB];
   int sa[2][MX ? NA : 1], sb[2][MX ? NB : 1];           // scale bytes of a stage: block 2 s + half in byte 2 s
   auto read_scales = [&](auto SET, int kt) __attribute__((always_inline)) -> void {
@@ -228,44 +216,74 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
     });
   };
 
+  // Two stages of the first tile set out; from then on the next tile's two do before
+  // a tile's epilogue.  (Their buffers' last readers are behind the last meeting; what
+  // is read after it is not used.)
+  place();
   fetch_scales(k_lo);
   fetch(a0, b0, k_lo);
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070);
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
   fetch(a1, b1, k_lo + 1);
-  read_scales(Int<0>{}, k_lo);
-  read(Int<0>{}, Int<0>{}, Int<0>{}, a0, b0);
-  int kt = k_lo;
-  for (; kt + 2 <= k_hi; kt += 2) {
-    stage(Int<0>{}, a0, b0, a1, b1, kt);
-    stage(Int<1>{}, a1, b1, a0, b0, kt + 1);
-  }
-  if (kt < k_hi) stage(Int<0>{}, a0, b0, a1, b1, kt);
-  __builtin_amdgcn_s_waitcnt(0x0070);                   // (no transfer outlives the workgroup's LDS)
-
-#pragma unroll 1
-  for (int t = 0; t < NA * NB; ++t) {                   // one copy of the epilogue for all blocks
-    float v[16];
+  for (;;) {
+    // the sums start from the bias (the first split's do; zeros past the last channel)
+    {
+      const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(g.f.bias), (short)0, g.f.bias && split == 0 ? g.n * 4 : 0, 0x00020000);
 #pragma unroll
-    for (int i = 0; i < NA; ++i)
+      for (int i = 0; i < NA; ++i) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
-        if (t == i * NB + j) {
+        for (int q = 0; q < 4; ++q) {
+          const f32x4_t t = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (n0 + wa * PA + 32 * i + 8 * q + 4 * half) * 4, 0, 0));
 #pragma unroll
-          for (int r = 0; r < 16; ++r) v[r] = acc[i][j][r];
+          for (int e = 0; e < 4; ++e) acc[i][0][4 * q + e] = t[e];
         }
-    const int64_t m = m0 + wb * PB + 32 * (t % NB) + (lane & 31);
-    const int n = n0 + wa * PA + 32 * (t / NB);
-    if (!g.part) {
-      finish_block(g.f, m, n, half, v);
-    } else if (m < g.m && n < g.n) {
-      float* p = g.part + ((int64_t)split * g.m + m) * g.ld + n + 4 * half;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<f32x4_t*>(p + 8 * q) = f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        for (int j = 1; j < NB; ++j) acc[i][j] = acc[i][0];
+      }
     }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read_scales(Int<0>{}, k_lo);
+    read(Int<0>{}, Int<0>{}, Int<0>{}, a0, b0);
+    int kt = k_lo;
+    for (; kt + 2 <= k_hi; kt += 2) {
+      stage(Int<0>{}, a0, b0, a1, b1, kt);
+      stage(Int<1>{}, a1, b1, a0, b0, kt + 1);
+    }
+    if (kt < k_hi) stage(Int<0>{}, a0, b0, a1, b1, kt);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);                 // (no transfer of this tile meets one of the next)
+    asm volatile("" ::: "memory");
+    const int em = m0, en = n0, es = split;
+    t += t_step;
+    const bool more = t < t_end;
+    if (more) {
+      place();
+      fetch_scales(k_lo);
+      fetch(a0, b0, k_lo);
+      fetch(a1, b1, k_lo + 1);
+    }
+    int l = lane;
+    asm("" : "+v"(l));
+    static_for<NA * NB>([&](auto U) __attribute__((always_inline)) -> void {
+      constexpr int i = decltype(U)::value / NB, j = decltype(U)::value % NB;
+      const int64_t m = em + wb * PB + 32 * j + (l & 31);
+      const int n = en + wa * PA + 32 * i;
+      float v[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) v[r] = acc[i][j][r];
+      if (PLAIN && g.part) {
+        if (m < g.m && n < g.n) {
+          float* p = g.part + ((int64_t)es * g.m + m) * g.ld + n + 4 * (l >> 5);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4_t*>(p + 8 * q) = f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        }
+      } else {
+        finish_block<PLAIN>(g.f, m, n, l >> 5, v);
+      }
+    });
+    if (!more) break;
   }
 #endif
 }
@@ -290,7 +308,7 @@ __global__ __launch_bounds__(256) void gemm_join(const float* __restrict__ part,
       }
     }
   }
-  finish_block(f, m, n0, half, v);
+  finish_block<false>(f, m, n0, half, v);
 }
 
 // ------------------------------------------------------------------ host
@@ -337,11 +355,18 @@ Choice choose(int64_t m, int64_t n, int64_t k, int type, bool exact) {
 }
 int64_t part_ld(int64_t n) { return (n + 31) / 32 * 32; }
 
-template <class T, bool AC, bool BC> st_status gemm_launch(const GemmArgs& g, int shape, hipStream_t st) {
-  const unsigned grid = (unsigned)((int64_t)g.tiles_a * g.tiles_b * g.splits);
-  if (shape == 0 && std::is_same<T, F32>::value) gemm<F32, AC, BC, 128, 128, 2, 2, 2><<<grid, 256, 0, st>>>(g);
-  else if (shape == 0) gemm<typename std::conditional<std::is_same<T, F32>::value, BF16, T>::type, AC, BC, 256, 256, 2, 4, 2><<<grid, 512, 0, st>>>(g);
-  else gemm<T, AC, BC, 128, 64, 2, 2, std::is_same<T, MX8>::value ? 2 : 3><<<grid, 256, 0, st>>>(g);
+// a workgroup per tile, or as many as the compute units hold
+int64_t gemm_grid(const GemmArgs& g, int per_cu) {
+  return std::min<int64_t>((int64_t)g.tiles_a * g.tiles_b * g.splits, (int64_t)kCus * per_cu);
+}
+
+template <class T, bool AC, bool BC, bool PLAIN> st_status gemm_launch(const GemmArgs& g, int shape, hipStream_t st) {
+  constexpr int type = std::is_same<T, F32>::value ? ST_F32 : std::is_same<T, BF16>::value ? ST_BF16 : ST_MX8;
+  const unsigned grid = (unsigned)gemm_grid(g, shape_of(type, shape).per_cu);
+  if constexpr (std::is_same<T, MX8X>::value) gemm<T, AC, BC, 128, 64, 2, 2, 2, PLAIN><<<grid, 256, 0, st>>>(g);
+  else if (shape == 1) gemm<T, AC, BC, 128, 64, 2, 2, std::is_same<T, MX8>::value ? 2 : 3, PLAIN><<<grid, 256, 0, st>>>(g);
+  else if constexpr (std::is_same<T, F32>::value) gemm<T, AC, BC, 128, 128, 2, 2, 2, PLAIN><<<grid, 256, 0, st>>>(g);
+  else gemm<T, AC, BC, 256, 256, 2, 4, 2, PLAIN><<<grid, 512, 0, st>>>(g);
   return launch_check("gemm");
 }
 
@@ -384,20 +409,20 @@ st_status product_launch(const Product& p, void* workspace, hipStream_t st) {
   g.ld = part_ld(p.n);
   g.part = c.splits > 1 ? static_cast<float*>(workspace) : nullptr;
   const int64_t ta = (p.n + h.ta - 1) / h.ta, tb = (p.m + h.tb - 1) / h.tb;
-  if (ta * tb * c.splits > max_blocks(256)) return fail(ST_ERR_UNSUPPORTED, "matrix product: too many tiles for one launch");
+  if (ta * tb * c.splits >= (1ll << 31)) return fail(ST_ERR_UNSUPPORTED, "matrix product: too many tiles");
   g.tiles_a = (int32_t)ta;
   g.tiles_b = (int32_t)tb;
+  const bool plain = g.part || (p.f.act == kActNone && p.f.pre.type < 0 && p.f.res.type < 0 && p.f.y.type != ST_MX8);
   st_status s;
-  if (exact) {
-    gemm<MX8X, false, false, 128, 64, 2, 2, 2><<<(unsigned)(ta * tb * c.splits), 256, 0, st>>>(g);
-    s = launch_check("gemm");
-  } else if (p.type == ST_MX8) s = gemm_launch<MX8, false, false>(g, c.shape, st);
-  else if (p.type == ST_BF16)
-    s = p.b_col ? gemm_launch<BF16, true, true>(g, c.shape, st)
-        : p.a_col ? gemm_launch<BF16, true, false>(g, c.shape, st) : gemm_launch<BF16, false, false>(g, c.shape, st);
+  if (p.type == ST_MX8)
+    s = exact ? (plain ? gemm_launch<MX8X, false, false, true>(g, c.shape, st) : gemm_launch<MX8X, false, false, false>(g, c.shape, st))
+              : (plain ? gemm_launch<MX8, false, false, true>(g, c.shape, st) : gemm_launch<MX8, false, false, false>(g, c.shape, st));
+  else if (p.type == ST_BF16)                           // (gradients' products are plain)
+    s = p.b_col ? gemm_launch<BF16, true, true, true>(g, c.shape, st) : p.a_col ? gemm_launch<BF16, true, false, true>(g, c.shape, st)
+        : plain ? gemm_launch<BF16, false, false, true>(g, c.shape, st) : gemm_launch<BF16, false, false, false>(g, c.shape, st);
   else
-    s = p.b_col ? gemm_launch<F32, true, true>(g, c.shape, st)
-        : p.a_col ? gemm_launch<F32, true, false>(g, c.shape, st) : gemm_launch<F32, false, false>(g, c.shape, st);
+    s = p.b_col ? gemm_launch<F32, true, true, true>(g, c.shape, st) : p.a_col ? gemm_launch<F32, true, false, true>(g, c.shape, st)
+        : plain ? gemm_launch<F32, false, false, true>(g, c.shape, st) : gemm_launch<F32, false, false, false>(g, c.shape, st);
   if (s != ST_OK || c.splits == 1) return s;
   const int bn = (int)(g.ld / 32);
   const int64_t blocks = (p.m + 31) / 32 * bn;
