@@ -299,7 +299,7 @@ struct Product {
   Finish f;
 };
 // Bytes of partial sums that a product of these sizes needs (0: none)
-size_t product_bytes(int64_t m, int64_t n, int64_t k, int type);
+size_t product_bytes(int64_t m, int64_t n, int64_t k, int type, bool cols);
 st_status product_launch(const Product& p, void* workspace, hipStream_t st);
 
 }  // namespace st

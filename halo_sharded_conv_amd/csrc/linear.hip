@@ -311,6 +311,129 @@ __global__ __launch_bounds__(256) void gemm_join(const float* __restrict__ part,
   finish_block<false>(f, m, n0, half, v);
 }
 
+// ------------------------------------------------------------------ few rows
+
+// Up to 64 rows of x: what counts is the weights' way from memory, once.  A
+// workgroup takes 32 channels of the output, its eight waves take turns along the
+// contraction in units of 128 bytes (a cache line of every weight row) and read
+// both operands' fragments straight into registers; their sums meet in LDS and are
+// added in the order of the waves.
+constexpr int kFewWaves = 8;
+
+template <class T> struct Unit;                         // fragments of a 128-byte unit, raw
+template <> struct Unit<BF16> { u32x4_t v[4]; };
+template <> struct Unit<F32> { u32x4_t v[4]; };
+template <> struct Unit<MX8> { u32x4_t v[4]; int scale; };
+template <> struct Unit<MX8X> { u32x4_t v[4]; int scale; };
+
+template <class T, int MB> __global__ __launch_bounds__(64 * kFewWaves, 2) void few_rows(const GemmArgs g) {
+#ifdef __HIP_DEVICE_COMPILE__
+  using P = Prod<T>;
+  constexpr bool EXACT = std::is_same<T, MX8X>::value, MX = std::is_same<T, MX8>::value || EXACT;
+  constexpr int DEEP = MB == 1 ? 4 : 2;                 // units of a wave in flight
+  __shared__ float4 sums[kFewWaves][MB][4][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, l32 = lane & 31;
+  const int split = blockIdx.x / g.tiles_a, n0 = (blockIdx.x - split * g.tiles_a) * 32;
+  const int u_lo = split * g.per_split, u_hi = min(g.stages, u_lo + g.per_split);
+
+  const auto ra = __builtin_amdgcn_make_buffer_rsrc(g.a.p + (int64_t)n0 * g.a.stride, (short)0, min(32, g.n - n0) * (int)g.a.stride, 0x00020000);
+  const auto rb = __builtin_amdgcn_make_buffer_rsrc(g.b.p, (short)0, g.m * (int)g.b.stride, 0x00020000);
+  const uint32_t at_a = l32 * (int)g.a.stride;
+  uint32_t at_b[MB];
+#pragma unroll
+  for (int j = 0; j < MB; ++j) at_b[j] = (32 * j + l32) * (int)g.b.stride;
+  // the 16-byte chunks of a unit that this lane holds, in the order of the steps
+  auto chunk = [&](int i) __attribute__((always_inline)) -> int {
+    return std::is_same<T, MX8>::value ? 4 * (i >> 1) + 2 * (i & 1) + half : EXACT ? 4 * (i >> 1) + 2 * half + (i & 1) : 2 * i + half;
+  };
+  auto load = [&](Unit<T>& f, auto rs, uint32_t row, int r, const Rows& o, const uint8_t* sp, int rows, int u) __attribute__((always_inline)) -> void {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int byte = u * 128 + chunk(i) * 16;
+      const uint32_t at = u < u_hi && byte < g.kbytes ? row + byte : kPastEnd;
+      f.v[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0));
+    }
+    if constexpr (MX) {
+      const auto rsc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(sp), (short)0, rows * (int)o.scale_stride, 0x00020000);
+      // (past the last block the codes are zero; a byte there may be NaN's)
+      const int blocks = g.blocks_k - 4 * u;
+      const uint32_t mask = blocks >= 4 ? 0xFFFFFFFFu : blocks <= 0 ? 0u : (1u << 8 * blocks) - 1;
+      const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(rsc, u < u_hi ? (uint32_t)(r * (int)o.scale_stride + 4 * u) : kPastEnd, 0, 0);
+      f.scale = (int)((w & mask) >> 8 * half);
+    }
+  };
+  auto frag = [&](const Unit<T>& f, auto S) __attribute__((always_inline)) -> auto {
+    constexpr int s = decltype(S)::value;
+    if constexpr (EXACT) return P::widen(Prod<MX8>::join(f.v[2 * s], f.v[2 * s + 1]), f.scale >> 16 * s & 255);
+    else if constexpr (MX) return P::join(f.v[2 * s], f.v[2 * s + 1]);
+    else return __builtin_bit_cast(typename P::Frag, f.v[s]);
+  };
+
+  f32x16 acc[MB];
+#pragma unroll
+  for (int j = 0; j < MB; ++j) acc[j] = f32x16{};
+  const uint8_t* spa = MX ? g.a.scales + (int64_t)n0 * g.a.scale_stride : nullptr;
+  for (int u0 = u_lo + wave; u0 < u_hi; u0 += DEEP * kFewWaves) {
+    Unit<T> ua[DEEP], ub[DEEP][MB];
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) {
+      load(ua[d], ra, at_a, l32, g.a, spa, min(32, g.n - n0), u0 + d * kFewWaves);
+#pragma unroll
+      for (int j = 0; j < MB; ++j) load(ub[d][j], rb, at_b[j], 32 * j + l32, g.b, g.b.scales, g.m, u0 + d * kFewWaves);
+    }
+    __builtin_amdgcn_sched_barrier(0);                  // (all on their way before the first is used)
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d)
+      static_for<P::STEPS>([&](auto S) __attribute__((always_inline)) -> void {
+        const auto fa = frag(ua[d], S);
+#pragma unroll
+        for (int j = 0; j < MB; ++j) {
+          int sa = 0, sb = 0;
+          if constexpr (MX) { sa = ua[d].scale; sb = ub[d][j].scale; }
+          acc[j] = P::template mul<decltype(S)::value>(fa, frag(ub[d][j], S), acc[j], sa, sb);
+        }
+      });
+  }
+#pragma unroll
+  for (int j = 0; j < MB; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sums[wave][j][q][lane] = float4{acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
+  __syncthreads();
+  if (wave >= MB) return;
+  float v[16];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float4 t = sums[0][wave][q][lane];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) {
+      const float4 x = sums[w][wave][q][lane];
+      t.x += x.x; t.y += x.y; t.z += x.z; t.w += x.w;
+    }
+    v[4 * q] = t.x; v[4 * q + 1] = t.y; v[4 * q + 2] = t.z; v[4 * q + 3] = t.w;
+  }
+  const int64_t m = 32 * wave + l32;
+  if (g.f.bias && split == 0) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int n = n0 + 8 * q + 4 * half;
+      float t[4];
+      load_some<F32, 4>(reinterpret_cast<const char*>(g.f.bias + n), g.n - n, t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * q + i] += t[i];
+    }
+  }
+  if (!g.part) {
+    finish_block<false>(g.f, m, n0, half, v);
+  } else if (m < g.m) {
+    float* p = g.part + ((int64_t)split * g.m + m) * g.ld + n0 + 4 * half;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<f32x4_t*>(p + 8 * q) = f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+  }
+#endif
+}
+
 // ------------------------------------------------------------------ host
 
 struct Shape {                        // tile and what a compute unit holds of it
@@ -323,16 +446,26 @@ inline const Shape& shape_of(int type, int s) { return kShapes[type == ST_F32][s
 constexpr int kCus = 256;
 
 struct Choice {
-  int shape, splits, per_split;
+  int shape, splits, per_split;       // shape 2: few_rows
 };
+constexpr int kFewRows = 64;
 
 // Tile shape and split of the contraction: the cheapest by rounds over the compute
 // units (a stage's time goes with the tile's area; a tile's start and end cost
 // as much as some stages) plus the partial sums' way through memory.
-// exact: 8-bit operands with an fp32 output, which the small tile alone has.
-Choice choose(int64_t m, int64_t n, int64_t k, int type, bool exact) {
+// exact: 8-bit operands with an fp32 output, which the small tile alone has.  cols:
+// the weights are read across their rows.
+Choice choose(int64_t m, int64_t n, int64_t k, int type, bool exact, bool cols) {
   const int kt = 128 / type_size(type);
   const int64_t stages = (k + kt - 1) / kt;
+  if (m <= kFewRows && !cols) {
+    // a unit per wave at least; splits where the channels leave compute units idle
+    const int64_t blocks = (n + 31) / 32;
+    int64_t splits = std::max<int64_t>(1, std::min<int64_t>(kCus / blocks, stages / (2 * kFewWaves)));
+    const int64_t per = (stages + splits - 1) / splits;
+    splits = (stages + per - 1) / per;
+    return Choice{2, (int)splits, (int)per};
+  }
   Choice best{};
   double least = INFINITY;
   for (int s = exact ? 1 : 0; s < 2; ++s) {
@@ -360,6 +493,13 @@ int64_t gemm_grid(const GemmArgs& g, int per_cu) {
   return std::min<int64_t>((int64_t)g.tiles_a * g.tiles_b * g.splits, (int64_t)kCus * per_cu);
 }
 
+template <class T> st_status few_launch(const GemmArgs& g, hipStream_t st) {
+  const unsigned grid = (unsigned)g.tiles_a * g.splits;
+  if (g.m <= 32) few_rows<T, 1><<<grid, 64 * kFewWaves, 0, st>>>(g);
+  else few_rows<T, 2><<<grid, 64 * kFewWaves, 0, st>>>(g);
+  return launch_check("few_rows");
+}
+
 template <class T, bool AC, bool BC, bool PLAIN> st_status gemm_launch(const GemmArgs& g, int shape, hipStream_t st) {
   constexpr int type = std::is_same<T, F32>::value ? ST_F32 : std::is_same<T, BF16>::value ? ST_BF16 : ST_MX8;
   const unsigned grid = (unsigned)gemm_grid(g, shape_of(type, shape).per_cu);
@@ -372,11 +512,11 @@ template <class T, bool AC, bool BC, bool PLAIN> st_status gemm_launch(const Gem
 
 }  // namespace
 
-size_t product_bytes(int64_t m, int64_t n, int64_t k, int type) {
+size_t product_bytes(int64_t m, int64_t n, int64_t k, int type, bool cols) {
   if (m <= 0 || n <= 0 || k <= 0) return 0;
   size_t most = 0;
   for (int exact = 0; exact <= (type == ST_MX8); ++exact) {
-    const Choice c = choose(m, n, k, type, exact);
+    const Choice c = choose(m, n, k, type, exact, cols);
     if (c.splits > 1) most = std::max(most, (size_t)c.splits * (size_t)m * (size_t)part_ld(n) * 4);
   }
   return most;
@@ -391,8 +531,9 @@ st_status product_launch(const Product& p, void* workspace, hipStream_t st) {
     return launch_check("gemm_join");
   }
   const bool exact = p.type == ST_MX8 && (p.f.y.type == ST_F32 || p.f.pre.type == ST_F32);
-  const Choice c = choose(p.m, p.n, p.k, p.type, exact);
-  const Shape& h = shape_of(p.type, c.shape);
+  const Choice c = choose(p.m, p.n, p.k, p.type, exact, p.a_col);
+  const bool few = c.shape == 2;
+  const Shape h = few ? Shape{32, kFewRows, 1} : shape_of(p.type, c.shape);
   const int es = type_size(p.type), kt = 128 / es;
   GemmArgs g{};
   g.a = p.a;
@@ -414,7 +555,10 @@ st_status product_launch(const Product& p, void* workspace, hipStream_t st) {
   g.tiles_b = (int32_t)tb;
   const bool plain = g.part || (p.f.act == kActNone && p.f.pre.type < 0 && p.f.res.type < 0 && p.f.y.type != ST_MX8);
   st_status s;
-  if (p.type == ST_MX8)
+  if (few)
+    s = exact ? few_launch<MX8X>(g, st) : p.type == ST_MX8 ? few_launch<MX8>(g, st)
+        : p.type == ST_BF16 ? few_launch<BF16>(g, st) : few_launch<F32>(g, st);
+  else if (p.type == ST_MX8)
     s = exact ? (plain ? gemm_launch<MX8X, false, false, true>(g, c.shape, st) : gemm_launch<MX8X, false, false, false>(g, c.shape, st))
               : (plain ? gemm_launch<MX8, false, false, true>(g, c.shape, st) : gemm_launch<MX8, false, false, false>(g, c.shape, st));
   else if (p.type == ST_BF16)                           // (gradients' products are plain)

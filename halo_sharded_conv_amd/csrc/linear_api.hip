@@ -161,8 +161,8 @@ Layout layout_of(int64_t rows, int64_t in, int64_t out, int type, bool backward)
   l.w = take(pad ? (size_t)out * ldk : 0);
   l.p = take(backward ? (size_t)rows * ldn : 0);
   l.sums = take(backward ? (size_t)grad_shape(rows, out).parts * (size_t)out * 4 : 0);
-  size_t part = product_bytes(rows, out, in, type);
-  if (backward) part = std::max(product_bytes(rows, in, out, type), product_bytes(out, in, rows, type));
+  size_t part = backward ? 0 : product_bytes(rows, out, in, type, false);
+  if (backward) part = std::max(product_bytes(rows, in, out, type, true), product_bytes(out, in, rows, type, true));
   l.parts = take(part);
   l.total = at;
   return l;
