@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import List, Optional, Sequence
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -47,11 +48,6 @@ class _Tokens(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
-class _Rows(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("stride", ctypes.c_int64),
-                ("scale_stride", ctypes.c_int64), ("type", ctypes.c_int32)]
-
-
 class _GnLayout(ctypes.Structure):
     _fields_ = [("partials_offset", ctypes.c_size_t), ("stats_offset", ctypes.c_size_t),
                 ("scales_offset", ctypes.c_size_t), ("ymax_offset", ctypes.c_size_t),
@@ -81,7 +77,8 @@ def _load() -> ctypes.CDLL:
         raise ImportError(f"two HIP runtimes are loaded ({runtimes}); import torch before any other HIP library")
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     PP = ctypes.POINTER(ctypes.c_void_p)
-    PI32, PT, PR = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(_Tokens), ctypes.POINTER(_Rows)
+    PI32, PT = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(_Tokens)
+    PR = ctypes.c_char_p                     # an st_rows, packed
     sig = {
         "st_version": (ctypes.c_char_p, []),
         "st_last_error": (ctypes.c_char_p, []),
@@ -894,10 +891,18 @@ _ROW_TYPES = {"f32": ST_F32, "bf16": ST_BF16, "mx8": ST_MX8}
 _ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 
 
+# An operand's st_rows as bytes: data, scales, stride, scale stride, type.  (Packed
+# by struct and passed as a pointer to the bytes: a third of the time of a ctypes
+# structure, of which a call takes up to six.)
+_PACK = struct.Struct("=QQqqi4x").pack
+
+
 class Mx8:
     """Rows of `channels` values in the 8-bit form: codes (bytes, [rows, at least
     channels]) and scales (bytes, [rows, at least a byte per 32 channels]).  The
     codes' row stride is a multiple of 16, the scales' of 4."""
+
+    __slots__ = ("codes", "scales", "channels", "rows")
 
     def __init__(self, codes, scales, channels: int):
         self.codes, self.scales, self.channels = codes, scales, int(channels)
@@ -907,10 +912,7 @@ class Mx8:
                 raise ShardConvError(2, f"Mx8: {what} are not bytes [rows, >= {least}] with contiguous rows")
         if codes.shape[0] != scales.shape[0]:
             raise ShardConvError(2, f"Mx8: {codes.shape[0]} rows of codes and {scales.shape[0]} of scales")
-
-    @property
-    def rows(self) -> int:
-        return int(self.codes.shape[0])
+        self.rows = int(codes.shape[0])
 
 
 def mx8_empty(rows: int, channels: int, device: str = "cuda") -> Mx8:
@@ -923,34 +925,41 @@ def mx8_empty(rows: int, channels: int, device: str = "cuda") -> Mx8:
 _ROW_DTYPES = {_torch().float32: ST_F32, _torch().bfloat16: ST_BF16}
 
 
-def _here(t, what: str) -> None:
+def _device() -> int:
+    return _torch()._C._cuda_getDevice()
+
+
+def _here(t, what: str, device: int) -> None:
     """The kernels run on the current device: operands of another one are refused."""
     if not getattr(t, "is_cuda", False):
         raise ShardConvError(1, f"{what}: expected a GPU tensor (no CPU fallback exists)")
-    if t.get_device() != _torch()._C._cuda_getDevice():
+    if t.get_device() != device:
         raise ShardConvError(1, f"{what}: on device {t.get_device()}, which is not the current one")
 
 
-def _rows(t, what: str, rows: int, channels: int):
+def _rows(t, call: str, name: str, rows: int, channels: int, device: int):
     """st_rows of a [rows, channels] tensor or an Mx8; None stays None."""
     if t is None:
         return None
-    if isinstance(t, Mx8):
-        if (t.rows, t.channels) != (rows, channels):
-            raise ShardConvError(2, f"{what}: expected {(rows, channels)}, got {(t.rows, t.channels)}")
-        _here(t.codes, what)
-        _here(t.scales, what)
-        return _Rows(t.codes.data_ptr(), t.scales.data_ptr(), t.codes.stride(0), t.scales.stride(0), ST_MX8)
-    _here(t, what)
+    if t.__class__ is Mx8:
+        if t.rows != rows or t.channels != channels:
+            raise ShardConvError(2, f"{call} {name}: expected {(rows, channels)}, got {(t.rows, t.channels)}")
+        c, s = t.codes, t.scales
+        if not (c.is_cuda and s.is_cuda and c.get_device() == device and s.get_device() == device):
+            _here(c, f"{call} {name}", device)
+            _here(s, f"{call} {name}", device)
+        return _PACK(c.data_ptr(), s.data_ptr(), c.stride(0), s.stride(0), ST_MX8)
+    if not (getattr(t, "is_cuda", False) and t.get_device() == device):
+        _here(t, f"{call} {name}", device)
     if t.shape != (rows, channels):
-        raise ShardConvError(2, f"{what}: expected {(rows, channels)}, got {tuple(t.shape)}")
+        raise ShardConvError(2, f"{call} {name}: expected {(rows, channels)}, got {tuple(t.shape)}")
     dt = _ROW_DTYPES.get(t.dtype)
     if dt is None:
-        raise ShardConvError(1, f"{what}: expected float32, bfloat16 or Mx8, got {t.dtype}")
+        raise ShardConvError(1, f"{call} {name}: expected float32, bfloat16 or Mx8, got {t.dtype}")
     st, sc = t.stride()
     if sc != 1 and channels > 1 and rows:
-        raise ShardConvError(2, f"{what}: channels must be contiguous")
-    return _Rows(t.data_ptr(), None, st, 0, dt)
+        raise ShardConvError(2, f"{call} {name}: channels must be contiguous")
+    return _PACK(t.data_ptr(), 0, st, 0, dt)
 
 
 def _shape(t, what: str):
@@ -969,16 +978,18 @@ def _act(act: str, what: str) -> int:
 
 def st_mx8_store(x, out: Mx8, stream=None) -> None:
     """x: [rows, channels], float32 or bfloat16, into the 8-bit form."""
+    dev = _device()
     n, c = _shape(x, "st_mx8_store x")
-    _check(lib.st_mx8_store(n, c, _rows(x, "st_mx8_store x", n, c), _rows(out, "st_mx8_store out", n, c), _stream(stream)),
+    _check(lib.st_mx8_store(n, c, _rows(x, "st_mx8_store", "x", n, c, dev), _rows(out, "st_mx8_store", "out", n, c, dev), _stream(stream)),
            "st_mx8_store")
 
 
 def st_mx8_load(x: Mx8, out, act: str = "none", stream=None) -> None:
     """act(x) into [rows, channels], float32 or bfloat16."""
+    dev = _device()
     n, c = _shape(x, "st_mx8_load x")
-    _check(lib.st_mx8_load(n, c, _rows(x, "st_mx8_load x", n, c), _act(act, "st_mx8_load"),
-                           _rows(out, "st_mx8_load out", n, c), _stream(stream)), "st_mx8_load")
+    _check(lib.st_mx8_load(n, c, _rows(x, "st_mx8_load", "x", n, c, dev), _act(act, "st_mx8_load"),
+                           _rows(out, "st_mx8_load", "out", n, c, dev), _stream(stream)), "st_mx8_load")
 
 
 def st_rmsnorm(x, residual, gamma, eps: float, total=None, y=None, y8: Optional[Mx8] = None, rstd=None, stream=None) -> None:
@@ -986,10 +997,11 @@ def st_rmsnorm(x, residual, gamma, eps: float, total=None, y=None, y8: Optional[
     8-bit form); rows of channels in float32 or bfloat16; gamma: C floats or
     None; rstd: a float per row or None."""
     what = "st_rmsnorm"
+    dev = _device()
     n, c = _shape(x, "st_rmsnorm x")
-    _check(lib.st_rmsnorm(n, c, _rows(x, "st_rmsnorm x", n, c), _rows(residual, "st_rmsnorm residual", n, c),
-                          _typed(gamma, "gamma", _FP32, 4 * c), float(eps), _rows(total, "st_rmsnorm total", n, c),
-                          _rows(y, "st_rmsnorm y", n, c), _rows(y8, "st_rmsnorm y8", n, c),
+    _check(lib.st_rmsnorm(n, c, _rows(x, "st_rmsnorm", "x", n, c, dev), _rows(residual, "st_rmsnorm", "residual", n, c, dev),
+                          _typed(gamma, "gamma", _FP32, 4 * c), float(eps), _rows(total, "st_rmsnorm", "total", n, c, dev),
+                          _rows(y, "st_rmsnorm", "y", n, c, dev), _rows(y8, "st_rmsnorm", "y8", n, c, dev),
                           _typed(rstd, "rstd", _FP32, 4 * n), _stream(stream)), what)
 
 
@@ -1001,11 +1013,12 @@ def st_rmsnorm_backward(s, dy, dtotal, gamma, rstd, dx, dgamma, workspace, strea
     """s: the forward call's total (a tensor, or the Mx8 it was kept in); dtotal:
     gradient at s from the residual stream, or None; dgamma: C floats or None."""
     what = "st_rmsnorm_backward"
+    dev = _device()
     n, c = _shape(s, "st_rmsnorm_backward s")
     ws, nb = _ws(workspace)
-    _check(lib.st_rmsnorm_backward(n, c, _rows(s, "st_rmsnorm_backward s", n, c), _rows(dy, "st_rmsnorm_backward dy", n, c),
-                                   _rows(dtotal, "st_rmsnorm_backward dtotal", n, c), _typed(gamma, "gamma", _FP32, 4 * c),
-                                   _typed(rstd, "rstd", _FP32, 4 * n), _rows(dx, "st_rmsnorm_backward dx", n, c),
+    _check(lib.st_rmsnorm_backward(n, c, _rows(s, "st_rmsnorm_backward", "s", n, c, dev), _rows(dy, "st_rmsnorm_backward", "dy", n, c, dev),
+                                   _rows(dtotal, "st_rmsnorm_backward", "dtotal", n, c, dev), _typed(gamma, "gamma", _FP32, 4 * c),
+                                   _typed(rstd, "rstd", _FP32, 4 * n), _rows(dx, "st_rmsnorm_backward", "dx", n, c, dev),
                                    _typed(dgamma, "dgamma", _FP32, 4 * c), ws, nb, _stream(stream)), what)
 
 
@@ -1019,23 +1032,25 @@ def st_linear(x, w, bias, y, act: str = "none", residual=None, pre=None, workspa
     type (float32, bfloat16, Mx8); y, pre: [rows, out] in any of the three, pre
     receives x w^T + bias; bias: float32 [out] or None."""
     what = "st_linear"
+    dev = _device()
     n, k = _shape(x, "st_linear x")
     m = _shape(w, "st_linear w")[0]
     ws, nb = _ws(workspace)
-    _check(lib.st_linear(n, k, m, _rows(x, "st_linear x", n, k), _rows(w, "st_linear w", m, k),
-                         _typed(bias, "bias", _FP32, 4 * m), _act(act, what), _rows(residual, "st_linear residual", n, m),
-                         _rows(y, "st_linear y", n, m), _rows(pre, "st_linear pre", n, m), ws, nb, _stream(stream)), what)
+    _check(lib.st_linear(n, k, m, _rows(x, "st_linear", "x", n, k, dev), _rows(w, "st_linear", "w", m, k, dev),
+                         _typed(bias, "bias", _FP32, 4 * m), _act(act, what), _rows(residual, "st_linear", "residual", n, m, dev),
+                         _rows(y, "st_linear", "y", n, m, dev), _rows(pre, "st_linear", "pre", n, m, dev), ws, nb, _stream(stream)), what)
 
 
 def st_linear_backward(x, w, dy, dx, dw, dbias, act: str = "none", pre=None, workspace=None, stream=None) -> None:
     """Gradients of st_linear at x, w and bias (each None: not computed).  x: w's
     type, or the Mx8 it was kept in; pre: as st_linear wrote it."""
     what = "st_linear_backward"
+    dev = _device()
     n, k = _shape(x, "st_linear_backward x")
     m = _shape(w, "st_linear_backward w")[0]
     ws, nb = _ws(workspace)
-    _check(lib.st_linear_backward(n, k, m, _rows(x, "st_linear_backward x", n, k), _rows(w, "st_linear_backward w", m, k),
-                                  _act(act, what), _rows(pre, "st_linear_backward pre", n, m),
-                                  _rows(dy, "st_linear_backward dy", n, m), _rows(dx, "st_linear_backward dx", n, k),
-                                  _rows(dw, "st_linear_backward dw", m, k), _typed(dbias, "dbias", _FP32, 4 * m), ws, nb,
+    _check(lib.st_linear_backward(n, k, m, _rows(x, "st_linear_backward", "x", n, k, dev), _rows(w, "st_linear_backward", "w", m, k, dev),
+                                  _act(act, what), _rows(pre, "st_linear_backward", "pre", n, m, dev),
+                                  _rows(dy, "st_linear_backward", "dy", n, m, dev), _rows(dx, "st_linear_backward", "dx", n, k, dev),
+                                  _rows(dw, "st_linear_backward", "dw", m, k, dev), _typed(dbias, "dbias", _FP32, 4 * m), ws, nb,
                                   _stream(stream)), what)

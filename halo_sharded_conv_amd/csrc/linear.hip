@@ -288,24 +288,37 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
 #endif
 }
 
-// Adds the splits' partial sums in order and finishes the blocks, one a wave
-__global__ __launch_bounds__(256) void gemm_join(const float* __restrict__ part, int splits, int64_t ld, Finish f, int blocks_n, int64_t blocks) {
+// Adds the splits' partial sums in order and finishes the blocks, a wave and a
+// workgroup each.  Four splits are on their way at once: with few blocks the pass
+// is as long as its loads are late (33 x 2048 in 4 splits: 5.7 -> 4.1 us us).
+__global__ __launch_bounds__(64) void gemm_join(const float* __restrict__ part, int splits, int64_t ld, Finish f, int blocks_n) {
   const int lane = threadIdx.x & 63, half = lane >> 5;
-  const int64_t blk = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (blk >= blocks) return;
-  const int64_t m = blk / blocks_n * 32 + (lane & 31);
-  const int n0 = (int)(blk % blocks_n) * 32;
+  const int64_t m = (int64_t)(blockIdx.x / blocks_n) * 32 + (lane & 31);
+  const int n0 = (int)(blockIdx.x % blocks_n) * 32;
   float v[16];
 #pragma unroll
   for (int r = 0; r < 16; ++r) v[r] = 0.f;
   if (m < f.rows) {
     const float* p = part + m * ld + n0 + 4 * half;
-    for (int s = 0; s < splits; ++s, p += (int64_t)f.rows * ld) {
+    const int64_t next = (int64_t)f.rows * ld;
+    int s = 0;
+    for (; s + 4 <= splits; s += 4, p += 4 * next) {
+      f32x4_t t[4][4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f32x4_t t = *reinterpret_cast<const f32x4_t*>(p + 8 * q);
-        v[4 * q] += t.x; v[4 * q + 1] += t.y; v[4 * q + 2] += t.z; v[4 * q + 3] += t.w;
-      }
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) t[i][q] = *reinterpret_cast<const f32x4_t*>(p + i * next + 8 * q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] += t[i][r / 4][r % 4];
+    }
+    for (; s < splits; ++s, p += next) {
+      f32x4_t t[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) t[q] = *reinterpret_cast<const f32x4_t*>(p + 8 * q);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) v[r] += t[r / 4][r % 4];
     }
   }
   finish_block<false>(f, m, n0, half, v);
@@ -441,47 +454,57 @@ struct Shape {                        // tile and what a compute unit holds of i
 };
 // large and small tile; fp32 (products a ninth as fast, twice the registers per
 // fragment) stays with 128 x 128
-constexpr Shape kShapes[2][2] = {{{256, 256, 1}, {128, 64, 3}}, {{128, 128, 2}, {128, 64, 3}}};
+constexpr Shape kShapes[2][3] = {{{256, 256, 1}, {128, 64, 3}, {64, 64, 4}}, {{128, 128, 2}, {128, 64, 3}, {64, 64, 4}}};
 inline const Shape& shape_of(int type, int s) { return kShapes[type == ST_F32][s]; }
+constexpr int kFewShape = 3;
 constexpr int kCus = 256;
 
 struct Choice {
-  int shape, splits, per_split;       // shape 2: few_rows
+  int shape, splits, per_split;
 };
 constexpr int kFewRows = 64;
 
-// Tile shape and split of the contraction: the cheapest by rounds over the compute
-// units (a stage's time goes with the tile's area; a tile's start and end cost
-// as much as some stages) plus the partial sums' way through memory.
-// exact: 8-bit operands with an fp32 output, which the small tile alone has.  cols:
+// What the choice between shapes and splits goes by, in microseconds, fitted to
+// measured products (96 x 2048 x 8192 to 458752 x 64 x 256, within a fifth of most):
+// a stage of one tile alone on a compute unit, a tile's share of a busy one, and
+// a tile's start and end.
+struct Pace {
+  double alone, busy, ends;
+};
+constexpr Pace kPace[2][3] = {{{1.0, 1.45, 7.0}, {0.48, 0.33, 3.0}, {0.42, 0.22, 2.0}}, {{2.0, 2.0, 7.0}, {1.0, 1.0, 3.0}, {0.55, 0.5, 2.0}}};
+
+// Tile shape and split of the contraction: the least time of the fullest compute
+// unit, with the partial sums' way through memory (7 TB/s, 5 us for the join).
+// exact: 8-bit operands with an fp32 output, which the middle tile alone has.  cols:
 // the weights are read across their rows.
 Choice choose(int64_t m, int64_t n, int64_t k, int type, bool exact, bool cols) {
   const int kt = 128 / type_size(type);
   const int64_t stages = (k + kt - 1) / kt;
   if (m <= kFewRows && !cols) {
-    // a unit per wave at least; splits where the channels leave compute units idle
+    // splits where the channels leave compute units idle, of two units a wave at least
     const int64_t blocks = (n + 31) / 32;
-    int64_t splits = std::max<int64_t>(1, std::min<int64_t>(kCus / blocks, stages / (2 * kFewWaves)));
+    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(kCus / blocks, stages / (2 * kFewWaves)));
     const int64_t per = (stages + splits - 1) / splits;
-    splits = (stages + per - 1) / per;
-    return Choice{2, (int)splits, (int)per};
+    return Choice{kFewShape, (int)((stages + per - 1) / per), (int)per};
   }
   Choice best{};
   double least = INFINITY;
-  for (int s = exact ? 1 : 0; s < 2; ++s) {
+  for (int s = exact ? 1 : 0; s < (exact ? 2 : 3); ++s) {
     const Shape& h = shape_of(type, s);
+    const Pace& p = kPace[type == ST_F32][s];
     const int64_t tiles = (n + h.ta - 1) / h.ta * ((m + h.tb - 1) / h.tb);
-    // microseconds of one stage of a full compute unit
-    const double stage = (type == ST_F32 ? 4.0 : 1.0) * h.ta * h.tb * h.per_cu / 65536.0 * (s ? 1.3 : 0.9);
-    for (int64_t splits = 1; splits <= 64; splits = splits < 4 ? splits + 1 : splits * 5 / 4) {
+    for (int64_t splits = 1; splits <= 512 && splits <= stages; splits = splits < 8 ? splits + 1 : splits * 9 / 8) {
       int64_t per = (stages + splits - 1) / splits;
       if (type == ST_MX8) per = (per + 3) / 4 * 4;       // (scale bytes come for four stages)
-      if (splits > 1 && ((stages + per - 1) / per != splits || per < 2)) continue;
-      const double rounds = std::ceil((double)tiles * splits / (kCus * h.per_cu));
-      const double fill = std::min(1.0, (double)tiles * splits / (kCus * h.per_cu));
-      double t = rounds * (per * stage * std::max(fill, 1.0 / h.per_cu) + 2.0);
-      if (splits > 1) t += 4.0 + (double)m * n * 4 * (splits * 2) / 4.0e6;
+      if ((stages + per - 1) / per != splits) continue;
+      const double all = (double)tiles * splits, fill = std::min(1.0, all / kCus);
+      const int64_t on = (tiles * splits + kCus - 1) / kCus;                 // tiles of the fullest unit
+      const double stage = s == 0 && type != ST_F32 ? p.alone + (p.busy - p.alone) * fill : p.busy;
+      double t = on <= h.per_cu ? per * std::max(p.alone, on * stage) + p.ends
+                                : on * per * stage + (on + h.per_cu - 1) / h.per_cu * p.ends;
+      if (splits > 1) t += 5.0 + (double)m * n * splits * 8 / 7.0e6;
       if (t < least) { least = t; best = Choice{s, (int)splits, (int)per}; }
+      if (tiles * splits > 8 * kCus) break;
     }
   }
   return best;
@@ -504,10 +527,18 @@ template <class T, bool AC, bool BC, bool PLAIN> st_status gemm_launch(const Gem
   constexpr int type = std::is_same<T, F32>::value ? ST_F32 : std::is_same<T, BF16>::value ? ST_BF16 : ST_MX8;
   const unsigned grid = (unsigned)gemm_grid(g, shape_of(type, shape).per_cu);
   if constexpr (std::is_same<T, MX8X>::value) gemm<T, AC, BC, 128, 64, 2, 2, 2, PLAIN><<<grid, 256, 0, st>>>(g);
+  else if (shape == 2) gemm<T, AC, BC, 64, 64, 2, 2, 4, PLAIN><<<grid, 256, 0, st>>>(g);
   else if (shape == 1) gemm<T, AC, BC, 128, 64, 2, 2, std::is_same<T, MX8>::value ? 2 : 3, PLAIN><<<grid, 256, 0, st>>>(g);
   else if constexpr (std::is_same<T, F32>::value) gemm<T, AC, BC, 128, 128, 2, 2, 2, PLAIN><<<grid, 256, 0, st>>>(g);
   else gemm<T, AC, BC, 256, 256, 2, 4, 2, PLAIN><<<grid, 512, 0, st>>>(g);
   return launch_check("gemm");
+}
+
+st_status join_launch(const float* part, int splits, const Finish& f, hipStream_t st) {
+  const int64_t blocks_n = part_ld(f.cols) / 32, blocks = ((int64_t)f.rows + 31) / 32 * blocks_n;
+  if (blocks > max_blocks(64)) return fail(ST_ERR_UNSUPPORTED, "matrix product: too many blocks for one launch");
+  gemm_join<<<(unsigned)blocks, 64, 0, st>>>(part, splits, part_ld(f.cols), f, (int)blocks_n);
+  return launch_check("gemm_join");
 }
 
 }  // namespace
@@ -523,16 +554,10 @@ size_t product_bytes(int64_t m, int64_t n, int64_t k, int type, bool cols) {
 }
 
 st_status product_launch(const Product& p, void* workspace, hipStream_t st) {
-  if (p.k == 0) {                                       // an empty sum: the epilogue of zeros
-    const int bn = (int)(part_ld(p.n) / 32);
-    const int64_t blocks = (p.m + 31) / 32 * bn;
-    if ((blocks + 3) / 4 > max_blocks(256)) return fail(ST_ERR_UNSUPPORTED, "matrix product: too many blocks for one launch");
-    gemm_join<<<(unsigned)((blocks + 3) / 4), 256, 0, st>>>(nullptr, 0, 0, p.f, bn, blocks);
-    return launch_check("gemm_join");
-  }
+  if (p.k == 0) return join_launch(nullptr, 0, p.f, st);       // an empty sum: the epilogue of zeros
   const bool exact = p.type == ST_MX8 && (p.f.y.type == ST_F32 || p.f.pre.type == ST_F32);
   const Choice c = choose(p.m, p.n, p.k, p.type, exact, p.a_col);
-  const bool few = c.shape == 2;
+  const bool few = c.shape == kFewShape;
   const Shape h = few ? Shape{32, kFewRows, 1} : shape_of(p.type, c.shape);
   const int es = type_size(p.type), kt = 128 / es;
   GemmArgs g{};
@@ -568,11 +593,7 @@ st_status product_launch(const Product& p, void* workspace, hipStream_t st) {
     s = p.b_col ? gemm_launch<F32, true, true, true>(g, c.shape, st) : p.a_col ? gemm_launch<F32, true, false, true>(g, c.shape, st)
         : plain ? gemm_launch<F32, false, false, true>(g, c.shape, st) : gemm_launch<F32, false, false, false>(g, c.shape, st);
   if (s != ST_OK || c.splits == 1) return s;
-  const int bn = (int)(g.ld / 32);
-  const int64_t blocks = (p.m + 31) / 32 * bn;
-  if ((blocks + 3) / 4 > max_blocks(256)) return fail(ST_ERR_UNSUPPORTED, "matrix product: too many blocks for one launch");
-  gemm_join<<<(unsigned)((blocks + 3) / 4), 256, 0, st>>>(g.part, c.splits, g.ld, g.f, bn, blocks);
-  return launch_check("gemm_join");
+  return join_launch(g.part, c.splits, p.f, st);
 }
 
 }  // namespace st

@@ -168,16 +168,16 @@ Layout layout_of(int64_t rows, int64_t in, int64_t out, int type, bool backward)
   return l;
 }
 
-st_status linear_sizes(int64_t rows, int64_t in, int64_t out, const std::string& me) {
-  if (rows < 0 || in < 1 || out < 1) return fail(ST_ERR_INVALID_ARG, me + ": negative rows, or no channels");
+st_status linear_sizes(int64_t rows, int64_t in, int64_t out, const char* me) {
+  if (rows < 0 || in < 1 || out < 1) return fail(ST_ERR_INVALID_ARG, std::string(me) + ": negative rows, or no channels");
   if (rows >= (1ll << 30) || in >= (1ll << 24) || out >= (1ll << 24))
-    return fail(ST_ERR_UNSUPPORTED, me + ": 2^30 rows or 2^24 channels");
+    return fail(ST_ERR_UNSUPPORTED, std::string(me) + ": 2^30 rows or 2^24 channels");
   return ST_OK;
 }
 // Tiles address 256 rows from one base by 32 bits
-st_status linear_stride(const Rows& r, const std::string& what) {
+st_status linear_stride(const Rows& r, const char* what) {
   if (r.type >= 0 && (r.stride >= (1 << 22) || r.scale_stride >= (1 << 22)))
-    return fail(ST_ERR_UNSUPPORTED, what + ": rows of 4 MiB or more apart");
+    return fail(ST_ERR_UNSUPPORTED, std::string(what) + ": rows of 4 MiB or more apart");
   return ST_OK;
 }
 
@@ -197,29 +197,29 @@ size_t st_linear_workspace_bytes(int64_t rows, int64_t in, int64_t out, int32_t 
 st_status st_linear(int64_t rows, int64_t in, int64_t out, const st_rows* x, const st_rows* w, const float* bias_or_null,
                     int32_t act, const st_rows* residual_or_null, const st_rows* y, const st_rows* pre_or_null,
                     void* workspace, size_t workspace_bytes, void* stream) {
-  const std::string me = "st_linear";
+  const char* const me = "st_linear";
   st_status s = linear_sizes(rows, in, out, me);
   if (s != ST_OK) return s;
-  if (act < ST_ACT_NONE || act > ST_ACT_SILU) return fail(ST_ERR_INVALID_ARG, me + ": unknown activation");
-  if (!aligned16(bias_or_null) || !aligned16(workspace)) return fail(ST_ERR_ALIGNMENT, me + ": bias or workspace not 16-byte aligned");
+  if (act < ST_ACT_NONE || act > ST_ACT_SILU) return fail(ST_ERR_INVALID_ARG, std::string(me) + ": unknown activation");
+  if (!aligned16(bias_or_null) || !aligned16(workspace)) return fail(ST_ERR_ALIGNMENT, std::string(me) + ": bias or workspace not 16-byte aligned");
   Product p{};
   p.f.pre = p.f.res = no_rows();
-  if ((s = rows_of(p.b, x, rows, in, kTakesAll, me + ": x")) != ST_OK) return s;
-  if ((s = rows_of(p.a, w, out, in, kTakesAll, me + ": w")) != ST_OK) return s;
-  if (p.a.type != p.b.type) return fail(ST_ERR_INVALID_ARG, me + ": x and w differ in type");
-  if ((s = rows_of(p.f.y, y, rows, out, kTakesAll, me + ": y")) != ST_OK) return s;
-  if (pre_or_null && (s = rows_of(p.f.pre, pre_or_null, rows, out, kTakesAll, me + ": pre")) != ST_OK) return s;
-  if (residual_or_null && (s = rows_of(p.f.res, residual_or_null, rows, out, kTakesFloat, me + ": residual")) != ST_OK) return s;
-  if ((s = linear_stride(p.b, me + ": x")) != ST_OK || (s = linear_stride(p.a, me + ": w")) != ST_OK) return s;
+  if ((s = rows_of(p.b, x, rows, in, kTakesAll, me, "x")) != ST_OK) return s;
+  if ((s = rows_of(p.a, w, out, in, kTakesAll, me, "w")) != ST_OK) return s;
+  if (p.a.type != p.b.type) return fail(ST_ERR_INVALID_ARG, std::string(me) + ": x and w differ in type");
+  if ((s = rows_of(p.f.y, y, rows, out, kTakesAll, me, "y")) != ST_OK) return s;
+  if (pre_or_null && (s = rows_of(p.f.pre, pre_or_null, rows, out, kTakesAll, me, "pre")) != ST_OK) return s;
+  if (residual_or_null && (s = rows_of(p.f.res, residual_or_null, rows, out, kTakesFloat, me, "residual")) != ST_OK) return s;
+  if ((s = linear_stride(p.b, me)) != ST_OK || (s = linear_stride(p.a, me)) != ST_OK) return s;
   if (rows > 0 && (meet(p.f.y, rows, out, p.b, rows, in) || meet(p.f.y, rows, out, p.a, out, in) ||
                    meet(p.f.pre, rows, out, p.b, rows, in) || meet(p.f.pre, rows, out, p.a, out, in) ||
                    meet(p.f.y, rows, out, p.f.pre, rows, out) || meet(p.f.pre, rows, out, p.f.res, rows, out) ||
                    (meet(p.f.y, rows, out, p.f.res, rows, out) && !same_rows(p.f.y, p.f.res))))
-    return fail(ST_ERR_BAD_SHAPE, me + ": an output overlaps an input or the other output");
+    return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": an output overlaps an input or the other output");
   p.type = p.a.type;
   const Layout l = layout_of(rows, in, out, p.type, false);
   if (rows > 0 && l.total > 0 && (!workspace || workspace_bytes < l.total))
-    return fail(ST_ERR_WORKSPACE, me + ": workspace missing or too small");
+    return fail(ST_ERR_WORKSPACE, std::string(me) + ": workspace missing or too small");
   if (rows == 0) return ok();
   const hipStream_t st = static_cast<hipStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
@@ -241,20 +241,20 @@ st_status st_linear_backward(int64_t rows, int64_t in, int64_t out, const st_row
                              const st_rows* pre_or_null, const st_rows* dy, const st_rows* dx_or_null,
                              const st_rows* dw_or_null, float* dbias_or_null, void* workspace, size_t workspace_bytes,
                              void* stream) {
-  const std::string me = "st_linear_backward";
+  const char* const me = "st_linear_backward";
   st_status s = linear_sizes(rows, in, out, me);
   if (s != ST_OK) return s;
-  if (act < ST_ACT_NONE || act > ST_ACT_SILU) return fail(ST_ERR_INVALID_ARG, me + ": unknown activation");
-  if (act != ST_ACT_NONE && !pre_or_null) return fail(ST_ERR_INVALID_ARG, me + ": an activation's gradient needs pre");
-  if (!aligned16(dbias_or_null) || !aligned16(workspace)) return fail(ST_ERR_ALIGNMENT, me + ": dbias or workspace not 16-byte aligned");
+  if (act < ST_ACT_NONE || act > ST_ACT_SILU) return fail(ST_ERR_INVALID_ARG, std::string(me) + ": unknown activation");
+  if (act != ST_ACT_NONE && !pre_or_null) return fail(ST_ERR_INVALID_ARG, std::string(me) + ": an activation's gradient needs pre");
+  if (!aligned16(dbias_or_null) || !aligned16(workspace)) return fail(ST_ERR_ALIGNMENT, std::string(me) + ": dbias or workspace not 16-byte aligned");
   Rows rx, rw, rdy, pre = no_rows(), dx = no_rows(), dw = no_rows();
-  if ((s = rows_of(rx, x, rows, in, kTakesAll, me + ": x")) != ST_OK) return s;
-  if ((s = rows_of(rw, w, out, in, kTakesFloat, me + ": w")) != ST_OK) return s;
-  if (rx.type != rw.type && rx.type != ST_MX8) return fail(ST_ERR_INVALID_ARG, me + ": x is neither in w's type nor in 8 bits");
-  if ((s = rows_of(rdy, dy, rows, out, kTakesFloat, me + ": dy")) != ST_OK) return s;
-  if (pre_or_null && (s = rows_of(pre, pre_or_null, rows, out, kTakesAll, me + ": pre")) != ST_OK) return s;
-  if (dx_or_null && (s = rows_of(dx, dx_or_null, rows, in, kTakesFloat, me + ": dx")) != ST_OK) return s;
-  if (dw_or_null && (s = rows_of(dw, dw_or_null, out, in, kTakesFloat, me + ": dw")) != ST_OK) return s;
+  if ((s = rows_of(rx, x, rows, in, kTakesAll, me, "x")) != ST_OK) return s;
+  if ((s = rows_of(rw, w, out, in, kTakesFloat, me, "w")) != ST_OK) return s;
+  if (rx.type != rw.type && rx.type != ST_MX8) return fail(ST_ERR_INVALID_ARG, std::string(me) + ": x is neither in w's type nor in 8 bits");
+  if ((s = rows_of(rdy, dy, rows, out, kTakesFloat, me, "dy")) != ST_OK) return s;
+  if (pre_or_null && (s = rows_of(pre, pre_or_null, rows, out, kTakesAll, me, "pre")) != ST_OK) return s;
+  if (dx_or_null && (s = rows_of(dx, dx_or_null, rows, in, kTakesFloat, me, "dx")) != ST_OK) return s;
+  if (dw_or_null && (s = rows_of(dw, dw_or_null, out, in, kTakesFloat, me, "dw")) != ST_OK) return s;
   for (const Rows* r : {&rx, &rw, &rdy, &pre})
     if ((s = linear_stride(*r, me)) != ST_OK) return s;
   struct Side { const Rows* r; int64_t rows, cols; };
@@ -262,11 +262,11 @@ st_status st_linear_backward(int64_t rows, int64_t in, int64_t out, const st_row
   const Side outs[2] = {{&dx, rows, in}, {&dw, out, in}};
   for (const Side& o : outs)
     for (const Side& i : ins)
-      if (meet(*o.r, o.rows, o.cols, *i.r, i.rows, i.cols)) return fail(ST_ERR_BAD_SHAPE, me + ": an output overlaps an input");
-  if (meet(dx, rows, in, dw, out, in)) return fail(ST_ERR_BAD_SHAPE, me + ": two outputs overlap");
+      if (meet(*o.r, o.rows, o.cols, *i.r, i.rows, i.cols)) return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": an output overlaps an input");
+  if (meet(dx, rows, in, dw, out, in)) return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": two outputs overlap");
   const int type = rw.type, es = type_size(type);
   const Layout l = layout_of(rows, in, out, type, true);
-  if (rows > 0 && (!workspace || workspace_bytes < l.total)) return fail(ST_ERR_WORKSPACE, me + ": workspace missing or too small");
+  if (rows > 0 && (!workspace || workspace_bytes < l.total)) return fail(ST_ERR_WORKSPACE, std::string(me) + ": workspace missing or too small");
   const hipStream_t st = static_cast<hipStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
 

@@ -94,9 +94,9 @@ template <class F> st_status mx_launches(MxArgs a, int64_t rows, int64_t channel
   return ST_OK;
 }
 
-st_status mx_sizes(int64_t rows, int64_t channels, const std::string& what) {
-  if (rows < 0 || channels < 1) return fail(ST_ERR_INVALID_ARG, what + ": negative rows or no channels");
-  if (rows >= (1ll << 31) || channels >= (1ll << 31) - 64) return fail(ST_ERR_UNSUPPORTED, what + ": 2^31 rows or channels");
+st_status mx_sizes(int64_t rows, int64_t channels, const char* what) {
+  if (rows < 0 || channels < 1) return fail(ST_ERR_INVALID_ARG, std::string(what) + ": negative rows or no channels");
+  if (rows >= (1ll << 31) || channels >= (1ll << 31) - 64) return fail(ST_ERR_UNSUPPORTED, std::string(what) + ": 2^31 rows or channels");
   return ST_OK;
 }
 
@@ -132,26 +132,26 @@ using namespace st;
 extern "C" {
 
 st_status st_mx8_store(int64_t rows, int64_t channels, const st_rows* x, const st_rows* out, void* stream) {
-  const std::string me = "st_mx8_store";
+  const char* const me = "st_mx8_store";
   st_status s = mx_sizes(rows, channels, me);
   if (s != ST_OK) return s;
   Rows rx, ro;
-  if ((s = rows_of(rx, x, rows, channels, kTakesFloat, me + ": x")) != ST_OK) return s;
-  if ((s = rows_of(ro, out, rows, channels, 1u << ST_MX8, me + ": out")) != ST_OK) return s;
-  if (rows_meet(rx, ro, rows, channels)) return fail(ST_ERR_BAD_SHAPE, me + ": x and out overlap");
+  if ((s = rows_of(rx, x, rows, channels, kTakesFloat, me, "x")) != ST_OK) return s;
+  if ((s = rows_of(ro, out, rows, channels, 1u << ST_MX8, me, "out")) != ST_OK) return s;
+  if (rows_meet(rx, ro, rows, channels)) return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": x and out overlap");
   if (rows == 0) return ok();
   return mx8_store_rows(rows, channels, rx, ro, static_cast<hipStream_t>(stream));
 }
 
 st_status st_mx8_load(int64_t rows, int64_t channels, const st_rows* x, int32_t act, const st_rows* out, void* stream) {
-  const std::string me = "st_mx8_load";
+  const char* const me = "st_mx8_load";
   st_status s = mx_sizes(rows, channels, me);
   if (s != ST_OK) return s;
-  if (act < ST_ACT_NONE || act > ST_ACT_SILU) return fail(ST_ERR_INVALID_ARG, me + ": unknown activation");
+  if (act < ST_ACT_NONE || act > ST_ACT_SILU) return fail(ST_ERR_INVALID_ARG, std::string(me) + ": unknown activation");
   Rows rx, ro;
-  if ((s = rows_of(rx, x, rows, channels, 1u << ST_MX8, me + ": x")) != ST_OK) return s;
-  if ((s = rows_of(ro, out, rows, channels, kTakesFloat, me + ": out")) != ST_OK) return s;
-  if (rows_meet(rx, ro, rows, channels)) return fail(ST_ERR_BAD_SHAPE, me + ": x and out overlap");
+  if ((s = rows_of(rx, x, rows, channels, 1u << ST_MX8, me, "x")) != ST_OK) return s;
+  if ((s = rows_of(ro, out, rows, channels, kTakesFloat, me, "out")) != ST_OK) return s;
+  if (rows_meet(rx, ro, rows, channels)) return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": x and out overlap");
   if (rows == 0) return ok();
   return mx8_load_rows(rows, channels, rx, act, ro, static_cast<hipStream_t>(stream));
 }

@@ -305,10 +305,10 @@ template <class TS> st_status rms_backward_launch(const RmsArgs& a, const RmsPic
   return fail(ST_ERR_UNSUPPORTED, "rms norm: no kernel for this width");
 }
 
-st_status rms_sizes(int64_t rows, int64_t channels, const std::string& me) {
-  if (rows < 0 || channels < 1) return fail(ST_ERR_INVALID_ARG, me + ": negative rows or no channels");
-  if (channels > kRmsMaxC) return fail(ST_ERR_UNSUPPORTED, me + ": more than 16384 channels");
-  if (rows >= (1ll << 31) - kRmsMaxParts) return fail(ST_ERR_UNSUPPORTED, me + ": 2^31 rows");
+st_status rms_sizes(int64_t rows, int64_t channels, const char* me) {
+  if (rows < 0 || channels < 1) return fail(ST_ERR_INVALID_ARG, std::string(me) + ": negative rows or no channels");
+  if (channels > kRmsMaxC) return fail(ST_ERR_UNSUPPORTED, std::string(me) + ": more than 16384 channels");
+  if (rows >= (1ll << 31) - kRmsMaxParts) return fail(ST_ERR_UNSUPPORTED, std::string(me) + ": 2^31 rows");
   return ST_OK;
 }
 
@@ -349,27 +349,27 @@ extern "C" {
 st_status st_rmsnorm(int64_t rows, int64_t channels, const st_rows* x, const st_rows* residual_or_null,
                      const float* gamma_or_null, float eps, const st_rows* total_or_null, const st_rows* y_or_null,
                      const st_rows* y8_or_null, float* rstd_or_null, void* stream) {
-  const std::string me = "st_rmsnorm";
+  const char* const me = "st_rmsnorm";
   st_status s = rms_sizes(rows, channels, me);
   if (s != ST_OK) return s;
-  if (!(eps >= 0.f) || !(eps < 3.0e38f)) return fail(ST_ERR_INVALID_ARG, me + ": eps must be finite and >= 0");
-  if (!aligned16(gamma_or_null) || !aligned16(rstd_or_null)) return fail(ST_ERR_ALIGNMENT, me + ": gamma or rstd not 16-byte aligned");
-  if (!total_or_null && !y_or_null && !y8_or_null && !rstd_or_null) return fail(ST_ERR_INVALID_ARG, me + ": no output");
+  if (!(eps >= 0.f) || !(eps < 3.0e38f)) return fail(ST_ERR_INVALID_ARG, std::string(me) + ": eps must be finite and >= 0");
+  if (!aligned16(gamma_or_null) || !aligned16(rstd_or_null)) return fail(ST_ERR_ALIGNMENT, std::string(me) + ": gamma or rstd not 16-byte aligned");
+  if (!total_or_null && !y_or_null && !y8_or_null && !rstd_or_null) return fail(ST_ERR_INVALID_ARG, std::string(me) + ": no output");
   RmsArgs a{};
   a.res = a.total = a.y = a.y8 = no_rows();
-  if ((s = rows_of(a.x, x, rows, channels, kTakesFloat, me + ": x")) != ST_OK) return s;
-  if (residual_or_null && (s = rows_of(a.res, residual_or_null, rows, channels, kTakesFloat, me + ": residual")) != ST_OK) return s;
-  if (total_or_null && (s = rows_of(a.total, total_or_null, rows, channels, kTakesFloat, me + ": total")) != ST_OK) return s;
-  if (y_or_null && (s = rows_of(a.y, y_or_null, rows, channels, kTakesFloat, me + ": y")) != ST_OK) return s;
-  if (y8_or_null && (s = rows_of(a.y8, y8_or_null, rows, channels, 1u << ST_MX8, me + ": y8")) != ST_OK) return s;
+  if ((s = rows_of(a.x, x, rows, channels, kTakesFloat, me, "x")) != ST_OK) return s;
+  if (residual_or_null && (s = rows_of(a.res, residual_or_null, rows, channels, kTakesFloat, me, "residual")) != ST_OK) return s;
+  if (total_or_null && (s = rows_of(a.total, total_or_null, rows, channels, kTakesFloat, me, "total")) != ST_OK) return s;
+  if (y_or_null && (s = rows_of(a.y, y_or_null, rows, channels, kTakesFloat, me, "y")) != ST_OK) return s;
+  if (y8_or_null && (s = rows_of(a.y8, y8_or_null, rows, channels, 1u << ST_MX8, me, "y8")) != ST_OK) return s;
   const Rows* in[2] = {&a.x, &a.res};
   const Rows* out[3] = {&a.total, &a.y, &a.y8};
   for (int i = 0; i < 3; ++i) {
     for (const Rows* r : in)
       if (rows_meet(*out[i], *r, rows, channels) && !(i == 0 && same_rows(*out[i], *r)))
-        return fail(ST_ERR_BAD_SHAPE, me + ": an output overlaps an input");
+        return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": an output overlaps an input");
     for (int j = 0; j < i; ++j)
-      if (rows_meet(*out[i], *out[j], rows, channels)) return fail(ST_ERR_BAD_SHAPE, me + ": two outputs overlap");
+      if (rows_meet(*out[i], *out[j], rows, channels)) return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": two outputs overlap");
   }
   if (rows == 0) return ok();
   a.rows = (int32_t)rows;
@@ -411,23 +411,23 @@ st_status st_rmsnorm_backward(int64_t rows, int64_t channels, const st_rows* s_,
                               const st_rows* dtotal_or_null, const float* gamma_or_null, const float* rstd,
                               const st_rows* dx, float* dgamma_or_null, void* workspace, size_t workspace_bytes,
                               void* stream) {
-  const std::string me = "st_rmsnorm_backward";
+  const char* const me = "st_rmsnorm_backward";
   st_status s = rms_sizes(rows, channels, me);
   if (s != ST_OK) return s;
-  if (rows > 0 && !rstd) return fail(ST_ERR_INVALID_ARG, me + ": NULL rstd");
+  if (rows > 0 && !rstd) return fail(ST_ERR_INVALID_ARG, std::string(me) + ": NULL rstd");
   if (!aligned16(gamma_or_null) || !aligned16(rstd) || !aligned16(dgamma_or_null) || !aligned16(workspace))
-    return fail(ST_ERR_ALIGNMENT, me + ": gamma, rstd, dgamma or workspace not 16-byte aligned");
+    return fail(ST_ERR_ALIGNMENT, std::string(me) + ": gamma, rstd, dgamma or workspace not 16-byte aligned");
   RmsArgs a{};
   a.res = a.y8 = no_rows();
-  if ((s = rows_of(a.x, s_, rows, channels, kTakesAll, me + ": s")) != ST_OK) return s;
-  if ((s = rows_of(a.total, dy, rows, channels, kTakesFloat, me + ": dy")) != ST_OK) return s;
-  if (dtotal_or_null && (s = rows_of(a.res, dtotal_or_null, rows, channels, kTakesFloat, me + ": dtotal")) != ST_OK) return s;
-  if ((s = rows_of(a.y, dx, rows, channels, kTakesFloat, me + ": dx")) != ST_OK) return s;
+  if ((s = rows_of(a.x, s_, rows, channels, kTakesAll, me, "s")) != ST_OK) return s;
+  if ((s = rows_of(a.total, dy, rows, channels, kTakesFloat, me, "dy")) != ST_OK) return s;
+  if (dtotal_or_null && (s = rows_of(a.res, dtotal_or_null, rows, channels, kTakesFloat, me, "dtotal")) != ST_OK) return s;
+  if ((s = rows_of(a.y, dx, rows, channels, kTakesFloat, me, "dx")) != ST_OK) return s;
   if (rows_meet(a.y, a.x, rows, channels) || (rows_meet(a.y, a.total, rows, channels) && !same_rows(a.y, a.total)) ||
       (rows_meet(a.y, a.res, rows, channels) && !same_rows(a.y, a.res)))
-    return fail(ST_ERR_BAD_SHAPE, me + ": dx overlaps an input");
+    return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": dx overlaps an input");
   if (dgamma_or_null && (!workspace || workspace_bytes < st_rmsnorm_backward_workspace_bytes(rows, channels)))
-    return fail(ST_ERR_WORKSPACE, me + ": workspace missing or too small");
+    return fail(ST_ERR_WORKSPACE, std::string(me) + ": workspace missing or too small");
   const hipStream_t st = static_cast<hipStream_t>(stream);
   a.channels = (int32_t)channels;
   float* partial = static_cast<float*>(workspace);

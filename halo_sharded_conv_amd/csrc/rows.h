@@ -24,29 +24,34 @@ constexpr int kMxBlock = ST_MX_BLOCK;
 // Checks of one operand of `rows` rows of `channels` channels.  Rows are 16-byte
 // aligned, or lie back to back (where one row's length is off that grid); `types`:
 // the bits 1 << type that the call takes.
-inline st_status rows_of(Rows& out, const st_rows* v, int64_t rows, int64_t channels, uint32_t types, const std::string& what) {
+// (messages are put together on failure only: a call's checks take a fraction of a
+// microsecond)
+inline st_status rows_fail(st_status s, const char* call, const char* name, const char* what) {
+  return fail(s, std::string(call) + ": " + name + ": " + what);
+}
+inline st_status rows_of(Rows& out, const st_rows* v, int64_t rows, int64_t channels, uint32_t types, const char* call, const char* name) {
   out = Rows{};
   out.type = -1;
-  if (!v) return fail(ST_ERR_INVALID_ARG, what + ": NULL operand");
-  if (v->type < 0 || v->type > ST_MX8 || !(types >> v->type & 1)) return fail(ST_ERR_INVALID_ARG, what + ": type not taken here");
+  if (!v) return rows_fail(ST_ERR_INVALID_ARG, call, name, "NULL operand");
+  if (v->type < 0 || v->type > ST_MX8 || !(types >> v->type & 1)) return rows_fail(ST_ERR_INVALID_ARG, call, name, "type not taken here");
   const int es = type_size(v->type);
-  if (rows > 0 && !v->data) return fail(ST_ERR_INVALID_ARG, what + ": NULL data");
-  if (!aligned16(v->data)) return fail(ST_ERR_ALIGNMENT, what + ": data not 16-byte aligned");
-  int64_t stride = rows > 1 ? v->stride : channels;           // (one row: its stride is not looked at)
+  if (rows > 0 && !v->data) return rows_fail(ST_ERR_INVALID_ARG, call, name, "NULL data");
+  if (!aligned16(v->data)) return rows_fail(ST_ERR_ALIGNMENT, call, name, "data not 16-byte aligned");
+  const int64_t stride = rows > 1 ? v->stride : channels;     // (one row: its stride is not looked at)
   if (rows > 1 && (stride < channels || stride > (1ll << 40)))
-    return fail(ST_ERR_BAD_SHAPE, what + ": row stride below the channels, or too large");
+    return rows_fail(ST_ERR_BAD_SHAPE, call, name, "row stride below the channels, or too large");
   if (rows > 1 && stride * es % 16 != 0 && (stride != channels || v->type == ST_MX8))
-    return fail(ST_ERR_ALIGNMENT, what + ": row stride neither a multiple of 16 bytes nor the row's own length");
+    return rows_fail(ST_ERR_ALIGNMENT, call, name, "row stride neither a multiple of 16 bytes nor the row's own length");
   out.p = static_cast<char*>(v->data);
   out.stride = stride * es;
   out.type = v->type;
   if (v->type == ST_MX8) {
     const int64_t blocks = (channels + kMxBlock - 1) / kMxBlock;
-    if (rows > 0 && !v->scales) return fail(ST_ERR_INVALID_ARG, what + ": NULL scales");
-    if (!aligned16(v->scales)) return fail(ST_ERR_ALIGNMENT, what + ": scales not 16-byte aligned");
-    int64_t ss = rows > 1 ? v->scale_stride : (blocks + 3) / 4 * 4;
-    if (rows > 1 && (ss < blocks || ss > (1ll << 40))) return fail(ST_ERR_BAD_SHAPE, what + ": scale stride below the blocks, or too large");
-    if (ss % 4 != 0) return fail(ST_ERR_ALIGNMENT, what + ": scale stride not a multiple of 4");
+    if (rows > 0 && !v->scales) return rows_fail(ST_ERR_INVALID_ARG, call, name, "NULL scales");
+    if (!aligned16(v->scales)) return rows_fail(ST_ERR_ALIGNMENT, call, name, "scales not 16-byte aligned");
+    const int64_t ss = rows > 1 ? v->scale_stride : (blocks + 3) / 4 * 4;
+    if (rows > 1 && (ss < blocks || ss > (1ll << 40))) return rows_fail(ST_ERR_BAD_SHAPE, call, name, "scale stride below the blocks, or too large");
+    if (ss % 4 != 0) return rows_fail(ST_ERR_ALIGNMENT, call, name, "scale stride not a multiple of 4");
     out.scales = v->scales;
     out.scale_stride = ss;
   }

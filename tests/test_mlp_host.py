@@ -15,7 +15,7 @@ AT = 1 << 40                                              # operands far apart, 
 
 def rows(i, stride, dtype=BF16, data=None, scales=None, ss=None):
     p = AT + (i << 36)
-    return hsc._Rows(p if data is None else data, (p + (1 << 35) if scales is None else scales) if dtype == MX8 else None, stride,
+    return hsc._PACK(p if data is None else data, (p + (1 << 35) if scales is None else scales) if dtype == MX8 else 0, stride,
                      (-(-stride // 128) * 4 if ss is None else ss) if dtype == MX8 else 0, dtype)
 
 
@@ -110,7 +110,7 @@ def test_workspace_queries():
 def test_binding_checks():
     t = torch.zeros(4, 64)
     with pytest.raises(hsc.ShardConvError):
-        hsc._rows(t, "x", 4, 64)                          # not on a GPU
+        hsc._rows(t, "call", "x", 4, 64, 0)                          # not on a GPU
     with pytest.raises(hsc.ShardConvError):
         hsc.Mx8(torch.zeros(4, 63, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8), 64)
     with pytest.raises(hsc.ShardConvError):
@@ -121,4 +121,4 @@ def test_binding_checks():
         hsc._act("tanh", "x")
     e = hsc.mx8_empty(3, 33, device="cpu")
     assert e.codes.shape == (3, 48) and e.scales.shape == (3, 4) and e.rows == 3
-    assert hsc._rows(None, "x", 4, 4) is None
+    assert hsc._rows(None, "call", "x", 4, 4, 0) is None
