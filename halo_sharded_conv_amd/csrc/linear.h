@@ -23,8 +23,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void* lds_void;
 typedef __attribute__((address_space(3))) v4s* lds_v4s;
 
-struct MX8 { static constexpr int kSize = 1; };
-
 constexpr uint32_t kPastEnd = 0x80000000u;      // past every num_records used: reads zeros
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base, int64_t bytes) {

@@ -80,45 +80,50 @@ struct GradArgs {
   int32_t cols, p_cols, act, lpr_log2, strips, parts;
 };
 
-template <bool ACT> __global__ __launch_bounds__(kGradThreads) void grad_pass(const GradArgs a) {
+// One group of 8 columns over its rows.  FULL: all 8 exist.
+template <int ACT, class TP, class TD, bool FULL> __device__ __forceinline__ void grad_rows(const GradArgs& a, int c, int n, int64_t first, int64_t step, float (&sum)[8]) {
+  const int p_n = a.p_cols - c;                         // (the padding past the columns gets zeros)
+  auto rows = [&](auto U, int64_t r0) __attribute__((always_inline)) -> void {
+    constexpr int kRows = decltype(U)::value;
+    float g[kRows][8], z[kRows][8];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t r = r0 + u * step;
+      load_some<TD, 8>(a.dy.p + r * a.dy.stride + (int64_t)c * TD::kSize, FULL ? 8 : n, g[u]);
+      if constexpr (ACT != kActNone) {
+        if constexpr (std::is_same<TP, MX8>::value) load_values<8>(a.pre, r, c, FULL ? 8 : n, z[u]);
+        else load_some<TP, 8>(a.pre.p + r * a.pre.stride + (int64_t)c * TP::kSize, FULL ? 8 : n, z[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t r = r0 + u * step;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (ACT != kActNone) g[u][i] *= slope_of<ACT>(z[u][i]);   // (columns that are not there: 0)
+        sum[i] += g[u][i];
+      }
+      if (a.p.type >= 0) store_some<8>(a.p.type, a.p.p + r * a.p.stride + (int64_t)c * (a.p.type == ST_F32 ? 4 : 2), FULL ? 8 : p_n, g[u]);
+    }
+  };
+  int64_t r = first;
+  for (; r + (kGradUnroll - 1) * step < a.rows; r += kGradUnroll * step) rows(std::integral_constant<int, kGradUnroll>{}, r);
+  for (; r < a.rows; r += step) rows(std::integral_constant<int, 1>{}, r);
+}
+
+template <int ACT, class TP, class TD> __global__ __launch_bounds__(kGradThreads) void grad_pass(const GradArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__
   __shared__ float acc[4][512];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lpr = 1 << a.lpr_log2, sub = lane & (lpr - 1), per = 4 * (64 >> a.lpr_log2);
   const int strip = blockIdx.x % a.strips, part = blockIdx.x / a.strips;
   const int c = (strip * lpr + sub) * 8, n = a.cols - c;
   const int64_t first = (int64_t)part * per + wave * (64 >> a.lpr_log2) + (lane >> a.lpr_log2), step = (int64_t)a.parts * per;
-  const int es = a.dy.type == ST_F32 ? 4 : 2;
   float sum[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) sum[i] = 0.f;
-  for (int64_t r0 = first; r0 < a.rows; r0 += step * kGradUnroll) {
-    float g[kGradUnroll][8], z[kGradUnroll][8];
-#pragma unroll
-    for (int u = 0; u < kGradUnroll; ++u) {
-      const int64_t r = r0 + u * step;
-      const int k = r < a.rows ? n : 0;
-      load_some<8>(a.dy.type, a.dy.p + r * a.dy.stride + (int64_t)c * es, k, g[u]);
-      if constexpr (ACT) {
-        if (a.pre.type == ST_MX8) load_values<8>(a.pre, r, c, k, z[u]);
-        else load_some<8>(a.pre.type, a.pre.p + r * a.pre.stride + (int64_t)c * (a.pre.type == ST_F32 ? 4 : 2), k, z[u]);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kGradUnroll; ++u) {
-      const int64_t r = r0 + u * step;
-      if constexpr (ACT) {
-        slopes(a.act, z[u]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[u][i] = i < n ? g[u][i] * z[u][i] : 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += g[u][i];
-      if (a.p.type >= 0 && r < a.rows) {
-        const int k = a.p_cols - c;                     // (the padding past the columns gets zeros)
-        if (k > 0) store_some<8>(a.p.type, a.p.p + r * a.p.stride + (int64_t)c * (a.p.type == ST_F32 ? 4 : 2), k, g[u]);
-      }
-    }
-  }
+  if (n >= 8) grad_rows<ACT, TP, TD, true>(a, c, n, first, step, sum);
+  else if (n > 0) grad_rows<ACT, TP, TD, false>(a, c, n, first, step, sum);
   if (!a.partial) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -130,6 +135,23 @@ template <bool ACT> __global__ __launch_bounds__(kGradThreads) void grad_pass(co
     const int col = strip * lpr * 8 + i;
     if (col < a.cols) a.partial[(int64_t)part * a.cols + col] = (acc[0][i] + acc[1][i]) + (acc[2][i] + acc[3][i]);
   }
+#endif
+}
+
+template <int ACT> st_status grad_launch(const GradArgs& g, unsigned grid, hipStream_t st) {
+#define GRAD_CASE(TP, TD) grad_pass<ACT, TP, TD><<<grid, kGradThreads, 0, st>>>(g)
+  const bool f = g.dy.type == ST_F32;
+  if constexpr (ACT == kActNone) {
+    if (f) GRAD_CASE(F32, F32); else GRAD_CASE(F32, BF16);
+  } else if (g.pre.type == ST_MX8) {
+    if (f) GRAD_CASE(MX8, F32); else GRAD_CASE(MX8, BF16);
+  } else if (g.pre.type == ST_BF16) {
+    if (f) GRAD_CASE(BF16, F32); else GRAD_CASE(BF16, BF16);
+  } else {
+    if (f) GRAD_CASE(F32, F32); else GRAD_CASE(F32, BF16);
+  }
+#undef GRAD_CASE
+  return launch_check("grad_pass");
 }
 
 struct GradShape {
@@ -292,9 +314,9 @@ st_status st_linear_backward(int64_t rows, int64_t in, int64_t out, const st_row
     }
     if (dbias_or_null) g.partial = reinterpret_cast<float*>(ws + l.sums);
     const unsigned grid = (unsigned)(gs.strips * gs.parts);
-    if (act != ST_ACT_NONE) grad_pass<true><<<grid, kGradThreads, 0, st>>>(g);
-    else grad_pass<false><<<grid, kGradThreads, 0, st>>>(g);
-    if ((s = launch_check("grad_pass")) != ST_OK) return s;
+    s = act == kActGelu ? grad_launch<kActGelu>(g, grid, st) : act == kActSilu ? grad_launch<kActSilu>(g, grid, st)
+        : act == kActRelu ? grad_launch<kActRelu>(g, grid, st) : grad_launch<kActNone>(g, grid, st);
+    if (s != ST_OK) return s;
     if (dbias_or_null && (s = add_rows_launch(g.partial, gs.parts, (int)out, dbias_or_null, st)) != ST_OK) return s;
   } else if (dbias_or_null) {
     if ((s = add_rows_launch(nullptr, 0, (int)out, dbias_or_null, st)) != ST_OK) return s;

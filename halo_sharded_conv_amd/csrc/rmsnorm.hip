@@ -160,10 +160,9 @@ template <int VEC, int NV, bool BLOCK> __global__ __launch_bounds__(kRmsThreads)
   }
 }
 
-// s, dy, dtotal -> dx, partial sums of dgamma.  TS: F32, BF16 or Mx8 (s as it was kept)
-struct Mx8 {};
+// s, dy, dtotal -> dx, partial sums of dgamma.  TS: F32, BF16 or MX8 (s as it was kept)
 template <class TS, int VEC> __device__ __forceinline__ void load_kept(const Rows& s, int64_t r, int c, int n, float (&x)[VEC]) {
-  if constexpr (std::is_same<TS, Mx8>::value) load_values<VEC>(s, r, c, n, x);
+  if constexpr (std::is_same<TS, MX8>::value) load_values<VEC>(s, r, c, n, x);
   else load_some<TS, VEC>(s.p + r * s.stride + (int64_t)c * TS::kSize, n, x);
 }
 
@@ -299,8 +298,10 @@ template <class TS> st_status rms_backward_launch(const RmsArgs& a, const RmsPic
   if (p.vec == V && p.nv == N && p.block == B) { rms_backward<TS, V, N, B><<<a.parts, kRmsThreads, 0, st>>>(a); return launch_check("rms_backward"); }
   RMS_CASE(8, 1, false) RMS_CASE(8, 2, false)
   RMS_CASE(8, 1, true) RMS_CASE(8, 2, true) RMS_CASE(8, 4, true) RMS_CASE(8, 8, true)
-  RMS_CASE(4, 1, false) RMS_CASE(4, 2, false) RMS_CASE(4, 4, false)
-  RMS_CASE(4, 2, true) RMS_CASE(4, 4, true) RMS_CASE(4, 8, true) RMS_CASE(4, 16, true)
+  if constexpr (std::is_same<TS, F32>::value) {         // (4 a lane: all sides fp32)
+    RMS_CASE(4, 1, false) RMS_CASE(4, 2, false) RMS_CASE(4, 4, false)
+    RMS_CASE(4, 2, true) RMS_CASE(4, 4, true) RMS_CASE(4, 8, true) RMS_CASE(4, 16, true)
+  }
 #undef RMS_CASE
   return fail(ST_ERR_UNSUPPORTED, "rms norm: no kernel for this width");
 }
@@ -445,7 +446,7 @@ st_status st_rmsnorm_backward(int64_t rows, int64_t channels, const st_rows* s_,
   const int rpb = rms_rows_per_block(pick, true);
   a.blocks = (int32_t)((rows + rpb - 1) / rpb);
   a.parts = std::min(rms_parts(rows), a.blocks);
-  s = a.x.type == ST_MX8 ? rms_backward_launch<Mx8>(a, pick, st)
+  s = a.x.type == ST_MX8 ? rms_backward_launch<MX8>(a, pick, st)
       : a.x.type == ST_F32 ? rms_backward_launch<F32>(a, pick, st) : rms_backward_launch<BF16>(a, pick, st);
   if (s != ST_OK || !dgamma_or_null) return s;
   return add_rows_launch(partial, a.parts, a.channels, dgamma_or_null, st);

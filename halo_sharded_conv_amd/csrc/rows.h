@@ -20,6 +20,7 @@ struct Rows {
 
 inline int type_size(int type) { return type == ST_F32 ? 4 : type == ST_BF16 ? 2 : 1; }
 constexpr int kMxBlock = ST_MX_BLOCK;
+struct MX8 { static constexpr int kSize = 1; };
 
 // Checks of one operand of `rows` rows of `channels` channels.  Rows are 16-byte
 // aligned, or lie back to back (where one row's length is off that grid); `types`:
@@ -193,7 +194,8 @@ template <bool SPECIAL> __device__ __forceinline__ uint32_t mx_codes(const float
   return (uint32_t)w;
 }
 __device__ __forceinline__ void mx_values(uint32_t w, int s, float* v) {
-  const float f = s == 0 ? 0x1p-127f : s == 255 ? __builtin_nanf("") : pow2_of(s);
+  // byte 0 is 2^-127 and 255 NaN: below and above what a float's exponent field says
+  const float f = (uint32_t)(s - 1) < 254u ? pow2_of(s) : s == 0 ? 0x1p-127f : __builtin_nanf("");
   const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
   v[0] = a.x * f; v[1] = a.y * f; v[2] = b.x * f; v[3] = b.y * f;
 }
@@ -286,10 +288,10 @@ template <int ACT> __device__ __forceinline__ float act_of(float z) {
   if constexpr (ACT == kActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
   if constexpr (ACT == kActGelu) {
     // z Phi(z) = max(z, 0) - |z| Q(|z|)
-    const float a = fminf(fabsf(z), 13.f);
-    return fmaf(-a * tail_poly(a), exp2_fast(-kHalfLog2e * z * z), fmaxf(z, 0.f));
+    const float a = __builtin_amdgcn_fmed3f(fabsf(z), 0.f, 13.f);
+    return fmaf(-a * tail_poly(a), exp2_fast(-kHalfLog2e * z * z), __builtin_amdgcn_fmed3f(z, 0.f, INFINITY));
   }
-  if constexpr (ACT == kActSilu) return fmaxf(z, -200.f) * rcp_fast(1.f + exp2_fast(-kLog2E * z));
+  if constexpr (ACT == kActSilu) return __builtin_amdgcn_fmed3f(z, -200.f, INFINITY) * rcp_fast(1.f + exp2_fast(-kLog2E * z));
   return z;
 }
 // derivative of the activation
@@ -297,11 +299,12 @@ template <int ACT> __device__ __forceinline__ float slope_of(float z) {
   if constexpr (ACT == kActRelu) return z > 0.f ? 1.f : 0.f;
   if constexpr (ACT == kActGelu) {
     // Phi(z) + z phi(z)
-    const float a = fminf(fabsf(z), 13.f), e = exp2_fast(-kHalfLog2e * z * z), q = tail_poly(a) * e;
-    return fmaf(fminf(fmaxf(z, -13.f), 13.f), e * kInvSqrt2Pi, z > 0.f ? 1.f - q : q);
+    const float a = __builtin_amdgcn_fmed3f(fabsf(z), 0.f, 13.f), e = exp2_fast(-kHalfLog2e * z * z);
+    const float tail = fmaf(-e, tail_poly(a), 0.5f);    // 1/2 - Q(|z|)
+    return fmaf(__builtin_amdgcn_fmed3f(z, -13.f, 13.f), e * kInvSqrt2Pi, 0.5f + copysignf(tail, z));
   }
   if constexpr (ACT == kActSilu) {
-    const float s = rcp_fast(1.f + exp2_fast(-kLog2E * z)), c = fminf(fmaxf(z, -200.f), 200.f);
+    const float s = rcp_fast(1.f + exp2_fast(-kLog2E * z)), c = __builtin_amdgcn_fmed3f(z, -200.f, 200.f);
     return s * fmaf(c, 1.f - s, 1.f);
   }
   return 1.f;
@@ -319,19 +322,6 @@ template <int N> __device__ __forceinline__ void activate(int act, float (&v)[N]
     for (int i = 0; i < N; ++i) v[i] = act_of<kActRelu>(v[i]);
   }
 }
-template <int N> __device__ __forceinline__ void slopes(int act, float (&v)[N]) {
-  if (act == kActGelu) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = slope_of<kActGelu>(v[i]);
-  } else if (act == kActSilu) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = slope_of<kActSilu>(v[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = slope_of<kActRelu>(v[i]);
-  }
-}
-
 // Launches that other operators make (mx8.hip)
 st_status mx8_store_rows(int64_t rows, int64_t channels, const Rows& x, const Rows& out, hipStream_t st);
 st_status mx8_load_rows(int64_t rows, int64_t channels, const Rows& x, int act, const Rows& out, hipStream_t st);
