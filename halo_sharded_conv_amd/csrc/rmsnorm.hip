@@ -27,7 +27,9 @@ namespace {
 
 constexpr int kRmsThreads = 256;
 constexpr int kRmsMaxC = 16384;
-constexpr int kRmsMaxParts = 1024;    // workgroups (partial rows) of the backward pass: four a CU
+// Workgroups (partial rows) of the backward pass, of which those of 16 waves take
+// half: four a CU (65536 rows of 2048 in bf16, a row each: 2048 of them 227 us, 1024 196)
+constexpr int kRmsMaxParts = 1024;
 
 struct RmsArgs {
   Rows x, res, total, y, y8;          // forward; backward: s, dtotal, -, dx, dy in x, res, -, y, total
@@ -42,9 +44,10 @@ template <int C> __device__ __forceinline__ float add_dpp(float v) {
   return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), C, 0xF, 0xF, false));
 }
 
-// sum over the lanes of one row (a power of two of them)
-template <bool BLOCK> __device__ __forceinline__ float row_sum(float v, int lpr, float* red) {
-  const int n = BLOCK ? 64 : lpr;
+// sum over the lanes of one row: a power of two of them, or (WAVES > 0) those of a
+// workgroup of so many waves
+template <int WAVES> __device__ __forceinline__ float row_sum(float v, int lpr, float* red) {
+  const int n = WAVES ? 64 : lpr;
   if (n > 1) v = add_dpp<0xB1>(v);                      // quad_perm 1 0 3 2
   if (n > 2) v = add_dpp<0x4E>(v);                      // quad_perm 2 3 0 1
   if (n > 4) v = add_dpp<0x141>(v);                     // row_half_mirror
@@ -57,12 +60,14 @@ template <bool BLOCK> __device__ __forceinline__ float row_sum(float v, int lpr,
     const u32x2_t r = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
     v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
   }
-  if constexpr (BLOCK) {
+  if constexpr (WAVES > 0) {
     const int wave = threadIdx.x >> 6;
     __syncthreads();                                    // the last sum's readers are done
     if ((threadIdx.x & 63) == 0) red[wave] = v;
     __syncthreads();
-    v = (red[0] + red[1]) + (red[2] + red[3]);
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; w += 4) v += (red[w] + red[w + 1]) + (red[w + 2] + red[w + 3]);
   }
   return v;
 }
@@ -73,7 +78,7 @@ constexpr int kRmsBackUnroll = 2;
 
 __device__ __forceinline__ int size_of(int type) { return type == ST_F32 ? 4 : 2; }
 
-template <int VEC, int NV, bool BLOCK> __global__ __launch_bounds__(kRmsThreads) void rms_forward(const RmsArgs a) {
+template <int VEC, int NV, bool BLOCK, bool EVEN> __global__ __launch_bounds__(kRmsThreads) void rms_forward(const RmsArgs a) {
   constexpr int U = BLOCK ? 1 : rms_unroll(NV * VEC);
   __shared__ float red[4];
   const int lpr = BLOCK ? kRmsThreads : 1 << a.lpr_log2;
@@ -81,29 +86,32 @@ template <int VEC, int NV, bool BLOCK> __global__ __launch_bounds__(kRmsThreads)
   const int C = a.channels;
   const int64_t r0 = (int64_t)blockIdx.x * (rp * U) + slot;
   float x[U][NV][VEC];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t r = r0 + u * rp;
-    const char* px = a.x.p + r * a.x.stride;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = (sub + k * lpr) * VEC;
-      load_some<VEC>(a.x.type, px + (int64_t)c * size_of(a.x.type), r < a.rows ? C - c : 0, x[u][k]);
-    }
-  }
-  if (a.res.type >= 0) {
+  {
+    Raw<VEC> xr[U][NV], rr[U][NV];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t r = r0 + u * rp;
-      const char* pr = a.res.p + r * a.res.stride;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int c = (sub + k * lpr) * VEC;
-        float t[VEC];
-        load_some<VEC>(a.res.type, pr + (int64_t)c * size_of(a.res.type), r < a.rows ? C - c : 0, t);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) x[u][k][i] += t[i];
+        const int c = (sub + k * lpr) * VEC, n = r < a.rows ? C - c : 0;
+        load_raw<EVEN, VEC>(a.x.type, a.x.p + r * a.x.stride + (int64_t)c * size_of(a.x.type), n, xr[u][k]);
+        if (a.res.type >= 0) load_raw<EVEN, VEC>(a.res.type, a.res.p + r * a.res.stride + (int64_t)c * size_of(a.res.type), n, rr[u][k]);
       }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < NV; ++k) unpack<VEC>(a.x.type, xr[u][k], x[u][k]);
+    if (a.res.type >= 0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          float t[VEC];
+          unpack<VEC>(a.res.type, rr[u][k], t);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) x[u][k][i] += t[i];
+        }
     }
   }
   if (a.total.type == ST_BF16) {                        // the norm is of s as it is kept
@@ -126,7 +134,7 @@ template <int VEC, int NV, bool BLOCK> __global__ __launch_bounds__(kRmsThreads)
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < VEC; ++i) t = fmaf(x[u][k][i], x[u][k][i], t);
-    rstd[u] = 1.f / sqrtf(row_sum<BLOCK>(t, lpr, red) / a.count + a.eps);
+    rstd[u] = 1.f / sqrtf(row_sum<BLOCK ? 4 : 0>(t, lpr, red) / a.count + a.eps);
   }
   if (a.rstd && sub == 0) {
 #pragma unroll
@@ -139,7 +147,11 @@ template <int VEC, int NV, bool BLOCK> __global__ __launch_bounds__(kRmsThreads)
     float g[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) g[i] = 1.f;
-    if (a.gamma) load_some<F32, VEC>(reinterpret_cast<const char*>(a.gamma + c), C - c, g);
+    if (a.gamma) {
+      Raw<VEC> t;
+      load_raw<EVEN, VEC>(ST_F32, reinterpret_cast<const char*>(a.gamma + c), C - c, t);
+      unpack<VEC>(ST_F32, t, g);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t r = r0 + u * rp;
@@ -147,30 +159,48 @@ template <int VEC, int NV, bool BLOCK> __global__ __launch_bounds__(kRmsThreads)
       float y[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) y[i] = x[u][k][i] * rstd[u] * g[i];
-      if (a.total.type >= 0 && n > 0) store_some<VEC, true>(a.total.type, a.total.p + r * a.total.stride + (int64_t)c * size_of(a.total.type), n, x[u][k]);
-      if (a.y.type >= 0 && n > 0) store_some<VEC, true>(a.y.type, a.y.p + r * a.y.stride + (int64_t)c * size_of(a.y.type), n, y);
+      if (a.total.type >= 0 && n > 0) store_some<VEC, true>(a.total.type, a.total.p + r * a.total.stride + (int64_t)c * size_of(a.total.type), EVEN ? VEC : n, x[u][k]);
+      if (a.y.type >= 0 && n > 0) store_some<VEC, true>(a.y.type, a.y.p + r * a.y.stride + (int64_t)c * size_of(a.y.type), EVEN ? VEC : n, y);
       if (a.y8.type >= 0) {                             // (every lane: a block's maximum crosses them)
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) top = max(top, i < n ? mx_bits(y[i]) : 0u);
+        for (int i = 0; i < VEC; ++i) top = max(top, EVEN || i < n ? mx_bits(y[i]) : 0u);   // (absent lanes hold zeros)
         const int s = mx_scale(block_max<VEC>(top));
-        store_codes<VEC>(a.y8, r, c, n, y, s);
+        store_codes<VEC>(a.y8, r, c, EVEN && n > 0 ? VEC : n, y, s);
       }
     }
   }
 }
 
 // s, dy, dtotal -> dx, partial sums of dgamma.  TS: F32, BF16 or MX8 (s as it was kept)
-template <class TS, int VEC> __device__ __forceinline__ void load_kept(const Rows& s, int64_t r, int c, int n, float (&x)[VEC]) {
-  if constexpr (std::is_same<TS, MX8>::value) load_values<VEC>(s, r, c, n, x);
-  else load_some<TS, VEC>(s.p + r * s.stride + (int64_t)c * TS::kSize, n, x);
+// a group of s as it was kept, before it is unpacked
+template <class TS, int VEC> struct Kept { Raw<VEC> r; int scale; };
+template <class TS, bool EVEN, int VEC> __device__ __forceinline__ void load_kept(const Rows& s, int64_t r, int c, int n, Kept<TS, VEC>& k) {
+  if constexpr (std::is_same<TS, MX8>::value) {
+    uint32_t w[VEC / 4];
+    k.scale = load_codes<VEC>(s, r, c, EVEN && n > 0 ? VEC : n, w);
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) k.r.w[i] = w[i];
+  } else {
+    load_raw<EVEN, VEC>(TS::kSize == 4 ? ST_F32 : ST_BF16, s.p + r * s.stride + (int64_t)c * TS::kSize, n, k.r);
+  }
+}
+template <class TS, int VEC> __device__ __forceinline__ void unpack_kept(const Kept<TS, VEC>& k, float (&x)[VEC]) {
+  if constexpr (std::is_same<TS, MX8>::value) {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) mx_values(k.r.w[i], k.scale, x + 4 * i);
+  } else {
+    unpack<VEC>(TS::kSize == 4 ? ST_F32 : ST_BF16, k.r, x);
+  }
 }
 
-template <class TS, int VEC, int NV, bool BLOCK> __global__ __launch_bounds__(kRmsThreads) void rms_backward(const RmsArgs a) {
-  constexpr int U = BLOCK ? 1 : kRmsBackUnroll;
-  __shared__ float red[4];
-  const int lpr = BLOCK ? kRmsThreads : 1 << a.lpr_log2;
-  const int sub = threadIdx.x & (lpr - 1), slot = threadIdx.x / lpr, rp = kRmsThreads / lpr;
+// WAVES: of a workgroup that holds a row; 0: rows in lane groups of four waves
+template <class TS, int VEC, int NV, int WAVES, bool EVEN> __global__ __launch_bounds__(WAVES ? 64 * WAVES : kRmsThreads) void rms_backward(const RmsArgs a) {
+  constexpr bool BLOCK = WAVES > 0;
+  constexpr int U = BLOCK ? 1 : kRmsBackUnroll, THREADS = BLOCK ? 64 * WAVES : kRmsThreads;
+  __shared__ float red[BLOCK ? WAVES : 4];
+  const int lpr = BLOCK ? THREADS : 1 << a.lpr_log2;
+  const int sub = threadIdx.x & (lpr - 1), slot = threadIdx.x / lpr, rp = THREADS / lpr;
   const int C = a.channels;
   const Rows &S = a.x, &DY = a.total, &DT = a.res, &DX = a.y;
   float g[NV][VEC], dg[NV][VEC];
@@ -179,11 +209,17 @@ template <class TS, int VEC, int NV, bool BLOCK> __global__ __launch_bounds__(kR
     const int c = (sub + k * lpr) * VEC;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) { g[k][i] = 1.f; dg[k][i] = 0.f; }
-    if (a.gamma) load_some<F32, VEC>(reinterpret_cast<const char*>(a.gamma + c), C - c, g[k]);
+    if (a.gamma) {
+      Raw<VEC> t;
+      load_raw<EVEN, VEC>(ST_F32, reinterpret_cast<const char*>(a.gamma + c), C - c, t);
+      unpack<VEC>(ST_F32, t, g[k]);
+    }
   }
   for (int blk = blockIdx.x; blk < a.blocks; blk += a.parts) {
     const int64_t r0 = (int64_t)blk * (rp * U) + slot;
-    float x[U][NV][VEC], dy[U][NV][VEC], dt[U][NV][VEC], rstd[U];
+    Kept<TS, VEC> sr[U][NV];
+    Raw<VEC> yr[U][NV], tr[U][NV];
+    float rstd[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t r = r0 + u * rp;
@@ -191,39 +227,43 @@ template <class TS, int VEC, int NV, bool BLOCK> __global__ __launch_bounds__(kR
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int c = (sub + k * lpr) * VEC, n = r < a.rows ? C - c : 0;
-        load_kept<TS, VEC>(S, r, c, n, x[u][k]);
-        load_some<VEC>(DY.type, DY.p + r * DY.stride + (int64_t)c * size_of(DY.type), n, dy[u][k]);
-        if (DT.type >= 0) {
-          load_some<VEC>(DT.type, DT.p + r * DT.stride + (int64_t)c * size_of(DT.type), n, dt[u][k]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) dt[u][k][i] = 0.f;
-        }
+        load_kept<TS, EVEN, VEC>(S, r, c, n, sr[u][k]);
+        load_raw<EVEN, VEC>(DY.type, DY.p + r * DY.stride + (int64_t)c * size_of(DY.type), n, yr[u][k]);
+        if (DT.type >= 0) load_raw<EVEN, VEC>(DT.type, DT.p + r * DT.stride + (int64_t)c * size_of(DT.type), n, tr[u][k]);
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t r = r0 + u * rp;
-      float t = 0.f;
+      float x[NV][VEC], dy[NV][VEC], t = 0.f;
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
+      for (int k = 0; k < NV; ++k) {
+        unpack_kept<TS, VEC>(sr[u][k], x[k]);
+        unpack<VEC>(DY.type, yr[u][k], dy[k]);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          const float xh = x[u][k][i] * rstd[u], d = dy[u][k][i];
-          x[u][k][i] = xh;
+          const float xh = x[k][i] * rstd[u], d = dy[k][i];
+          x[k][i] = xh;
           dg[k][i] = fmaf(d, xh, dg[k][i]);
-          dy[u][k][i] = d * g[k][i];
-          t = fmaf(dy[u][k][i], xh, t);
+          dy[k][i] = d * g[k][i];
+          t = fmaf(dy[k][i], xh, t);
         }
-      t = row_sum<BLOCK>(t, lpr, red) / a.count;
+      }
+      t = row_sum<WAVES>(t, lpr, red) / a.count;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int c = (sub + k * lpr) * VEC, n = r < a.rows ? C - c : 0;
         if (n <= 0) continue;
-        float dx[VEC];
+        float dx[VEC], dt[VEC];
+        if (DT.type >= 0) {
+          unpack<VEC>(DT.type, tr[u][k], dt);
+        } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) dx[i] = fmaf(rstd[u], dy[u][k][i] - x[u][k][i] * t, dt[u][k][i]);
-        store_some<VEC, true>(DX.type, DX.p + r * DX.stride + (int64_t)c * size_of(DX.type), n, dx);
+          for (int i = 0; i < VEC; ++i) dt[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) dx[i] = fmaf(rstd[u], dy[k][i] - x[k][i] * t, dt[i]);
+        store_some<VEC, true>(DX.type, DX.p + r * DX.stride + (int64_t)c * size_of(DX.type), EVEN ? VEC : n, dx);
       }
     }
   }
@@ -256,15 +296,16 @@ template <class TS, int VEC, int NV, bool BLOCK> __global__ __launch_bounds__(kR
 struct RmsPick {                      // how a row is held
   int vec, nv, lpr_log2;
   bool block;
+  int waves;                          // backward: of the workgroup that holds a row (0: lane groups)
 };
 
-// Whole rows per wave while a lane holds at most 64 values forward, 16 backward
-// (s, dy, dtotal, gamma and the column sums); at least the lanes of one block of 32
-RmsPick rms_pick(int C, bool wide, bool backward) {
+// Forward: whole rows per wave while a lane holds at most 64 values (32 with an fp32
+// operand), by a workgroup beyond.  At least the lanes of one block of 32.
+RmsPick rms_pick_forward(int C, bool wide) {
   RmsPick p{};
   p.vec = wide ? 8 : 4;
   const int nvec = (C + p.vec - 1) / p.vec;
-  const int most = (backward ? 16 : wide ? 64 : 32) / p.vec;
+  const int most = (wide ? 64 : 32) / p.vec;
   p.block = nvec > 64 * most;
   const int lanes = p.block ? 256 : 64;
   const int need = (nvec + lanes - 1) / lanes;
@@ -273,6 +314,22 @@ RmsPick rms_pick(int C, bool wide, bool backward) {
   int l = p.vec == 8 ? 2 : 3;
   while ((1 << l) < lanes && (1 << l) < nvec) ++l;
   p.lpr_log2 = p.block ? 8 : l;
+  return p;
+}
+// Backward: few values a lane, so that many waves fit a SIMD: rows by a wave's lanes up
+// to 1024 channels (two vectors of 8 a lane; 512 at 4), by 4, 8 or 16 waves beyond
+// (65536 x 1000 in bf16: by a wave 105 us, by four 113; 8192 x 8192: four vectors a
+// lane of four waves 163 us, one a lane of sixteen 105; 65536 x 500 in fp32: two vectors
+// of 4 a lane 104 us, by four waves 98).
+RmsPick rms_pick_backward(int C, bool wide) {
+  RmsPick p{};
+  p.vec = wide ? 8 : 4;
+  const int nvec = (C + p.vec - 1) / p.vec;
+  p.block = nvec > (wide ? 128 : 64);
+  p.waves = !p.block ? 0 : nvec <= 256 ? 4 : nvec <= 512 ? 8 : 16;
+  p.nv = 1;
+  while (p.nv * (p.block ? 64 * p.waves : 64) < nvec) p.nv *= 2;
+  while ((1 << p.lpr_log2) < nvec && p.lpr_log2 < 6) ++p.lpr_log2;
   return p;
 }
 
@@ -284,7 +341,11 @@ int rms_parts(int64_t rows) { return (int)std::max<int64_t>(1, std::min<int64_t>
 
 st_status rms_forward_launch(const RmsArgs& a, const RmsPick& p, int blocks, hipStream_t st) {
 #define RMS_CASE(V, N, B) \
-  if (p.vec == V && p.nv == N && p.block == B) { rms_forward<V, N, B><<<blocks, kRmsThreads, 0, st>>>(a); return launch_check("rms_forward"); }
+  if (p.vec == V && p.nv == N && p.block == B) { \
+    if (a.channels % V == 0) rms_forward<V, N, B, true><<<blocks, kRmsThreads, 0, st>>>(a); \
+    else rms_forward<V, N, B, false><<<blocks, kRmsThreads, 0, st>>>(a); \
+    return launch_check("rms_forward"); \
+  }
   RMS_CASE(8, 1, false) RMS_CASE(8, 2, false) RMS_CASE(8, 4, false) RMS_CASE(8, 8, false)
   RMS_CASE(8, 4, true) RMS_CASE(8, 8, true)
   RMS_CASE(4, 1, false) RMS_CASE(4, 2, false) RMS_CASE(4, 4, false) RMS_CASE(4, 8, false)
@@ -294,13 +355,15 @@ st_status rms_forward_launch(const RmsArgs& a, const RmsPick& p, int blocks, hip
 }
 
 template <class TS> st_status rms_backward_launch(const RmsArgs& a, const RmsPick& p, hipStream_t st) {
-#define RMS_CASE(V, N, B) \
-  if (p.vec == V && p.nv == N && p.block == B) { rms_backward<TS, V, N, B><<<a.parts, kRmsThreads, 0, st>>>(a); return launch_check("rms_backward"); }
-  RMS_CASE(8, 1, false) RMS_CASE(8, 2, false)
-  RMS_CASE(8, 1, true) RMS_CASE(8, 2, true) RMS_CASE(8, 4, true) RMS_CASE(8, 8, true)
+#define RMS_CASE(V, N, W) \
+  if (p.vec == V && p.nv == N && p.waves == W) { \
+    if (a.channels % V == 0) rms_backward<TS, V, N, W, true><<<a.parts, W ? 64 * W : kRmsThreads, 0, st>>>(a); \
+    else rms_backward<TS, V, N, W, false><<<a.parts, W ? 64 * W : kRmsThreads, 0, st>>>(a); \
+    return launch_check("rms_backward"); \
+  }
+  RMS_CASE(8, 1, 0) RMS_CASE(8, 2, 0) RMS_CASE(8, 1, 4) RMS_CASE(8, 1, 8) RMS_CASE(8, 1, 16) RMS_CASE(8, 2, 16)
   if constexpr (std::is_same<TS, F32>::value) {         // (4 a lane: all sides fp32)
-    RMS_CASE(4, 1, false) RMS_CASE(4, 2, false) RMS_CASE(4, 4, false)
-    RMS_CASE(4, 2, true) RMS_CASE(4, 4, true) RMS_CASE(4, 8, true) RMS_CASE(4, 16, true)
+    RMS_CASE(4, 1, 0) RMS_CASE(4, 1, 4) RMS_CASE(4, 1, 8) RMS_CASE(4, 1, 16) RMS_CASE(4, 2, 16) RMS_CASE(4, 4, 16)
   }
 #undef RMS_CASE
   return fail(ST_ERR_UNSUPPORTED, "rms norm: no kernel for this width");
@@ -382,7 +445,7 @@ st_status st_rmsnorm(int64_t rows, int64_t channels, const st_rows* x, const st_
   // 8 values a lane only where no operand is fp32: with one, 4 keep its accesses dense
   bool wide = true;
   for (const Rows* r : {&a.x, &a.res, &a.total, &a.y}) wide = wide && r->type != ST_F32;
-  const RmsPick pick = rms_pick((int)channels, wide, false);
+  const RmsPick pick = rms_pick_forward((int)channels, wide);
   a.lpr_log2 = pick.lpr_log2;
   const int rpb = rms_rows_per_block(pick, false);
   // launches of fewer than 2^32 threads, whole workgroups of rows each
@@ -441,11 +504,11 @@ st_status st_rmsnorm_backward(int64_t rows, int64_t channels, const st_rows* s_,
   // 8 values a lane with any side below 32 bits, as the layer norm's backward pass
   bool wide = false;
   for (const Rows* r : {&a.x, &a.res, &a.total, &a.y}) wide = wide || (r->type >= 0 && r->type != ST_F32);
-  const RmsPick pick = rms_pick(a.channels, wide, true);
+  const RmsPick pick = rms_pick_backward(a.channels, wide);
   a.lpr_log2 = pick.lpr_log2;
   const int rpb = rms_rows_per_block(pick, true);
   a.blocks = (int32_t)((rows + rpb - 1) / rpb);
-  a.parts = std::min(rms_parts(rows), a.blocks);
+  a.parts = std::min(std::min(rms_parts(rows), pick.waves == 16 ? kRmsMaxParts / 2 : kRmsMaxParts), a.blocks);
   s = a.x.type == ST_MX8 ? rms_backward_launch<MX8>(a, pick, st)
       : a.x.type == ST_F32 ? rms_backward_launch<F32>(a, pick, st) : rms_backward_launch<BF16>(a, pick, st);
   if (s != ST_OK || !dgamma_or_null) return s;

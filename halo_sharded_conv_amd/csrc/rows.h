@@ -130,6 +130,46 @@ template <int VEC> __device__ __forceinline__ void load_some(int type, const cha
   else load_some<BF16, VEC>(p, n, x);
 }
 
+// A group as it lies in memory, unpacked when it is used: a load that is unpacked
+// where its type is looked at would be waited for there, one after the other.
+// EVEN: groups are whole or absent (the row's length is a multiple of VEC).
+template <int VEC> struct Raw { uint32_t w[VEC]; };
+template <bool EVEN, int VEC> __device__ __forceinline__ void load_raw(int type, const char* p, int n, Raw<VEC>& r) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) r.w[i] = 0;
+  if (EVEN ? n > 0 : n >= VEC) {
+    if (VEC == 8 || type == ST_F32) {
+      const u32x4_t t = *reinterpret_cast<const u32x4_any*>(p);
+      r.w[0] = t[0]; r.w[1] = t[1]; r.w[2] = t[2]; r.w[3] = t[3];
+    } else {
+      const u32x2_t t = *reinterpret_cast<const u32x2_any*>(p);
+      r.w[0] = t[0]; r.w[1] = t[1];
+    }
+    if constexpr (VEC == 8) {
+      if (type == ST_F32) {
+        const u32x4_t t = *reinterpret_cast<const u32x4_any*>(p + 16);
+        r.w[4] = t[0]; r.w[5] = t[1]; r.w[6] = t[2]; r.w[7] = t[3];
+      }
+    }
+  } else if constexpr (!EVEN) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (i < n) {
+        if (type == ST_F32) r.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        else r.w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
+      }
+  }
+}
+template <int VEC> __device__ __forceinline__ void unpack(int type, const Raw<VEC>& r, float (&x)[VEC]) {
+  if (type == ST_F32) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) x[i] = __uint_as_float(r.w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) { x[2 * i] = bf16_lo(r.w[i]); x[2 * i + 1] = bf16_hi(r.w[i]); }
+  }
+}
+
 template <int VEC, bool NT = false> __device__ __forceinline__ void store_some(int type, char* p, int n, const float (&x)[VEC]) {
   if (type == ST_F32) {
     if (n >= VEC) {
