@@ -786,7 +786,7 @@ typedef struct st_rows {
 /*
  * st_mx8_store - rows in fp32 or bf16 to the 8-bit form: activations kept until
  * the backward pass, weights and inputs of an 8-bit product.
- *   rows, channels   rows >= 0 (0: nothing is done), channels >= 1, both below 2^31
+ *   rows, channels   rows >= 0 (0: nothing is done) and below 2^31, channels 1 .. 2^31 - 65
  * A block's scale is the smallest k with max |x| <= 448 * 2^k over its finite
  * values (k of -126 .. 127), the codes are x * 2^-k rounded to nearest even, so
  * that no finite value saturates; NaN and infinities become a NaN code (there are two).
@@ -795,7 +795,8 @@ typedef struct st_rows {
  * rounded up to 2^128 comes back as infinity), through
  * an activation if act is not ST_ACT_NONE: out = act(x).
  * x and out must not overlap.
- * Errors of both: ST_ERR_INVALID_ARG, ST_ERR_BAD_SHAPE, ST_ERR_ALIGNMENT, ST_ERR_HIP.
+ * Errors of both: ST_ERR_INVALID_ARG, ST_ERR_BAD_SHAPE, ST_ERR_UNSUPPORTED (larger),
+ * ST_ERR_ALIGNMENT, ST_ERR_HIP.
  */
 st_status st_mx8_store(int64_t rows, int64_t channels, const st_rows* x, const st_rows* out, void* stream);
 st_status st_mx8_load(int64_t rows, int64_t channels, const st_rows* x, int32_t act, const st_rows* out, void* stream);
@@ -827,7 +828,8 @@ st_status st_mx8_load(int64_t rows, int64_t channels, const st_rows* x, int32_t 
  *   workspace       >= st_rmsnorm_backward_workspace_bytes(rows, channels) bytes
  * dgamma is summed in fp32 in an order fixed by the sizes and types (no atomics).
  * Errors of both: ST_ERR_INVALID_ARG, ST_ERR_BAD_SHAPE (outputs that overlap an
- * input or one another), ST_ERR_UNSUPPORTED (more than 16384 channels, 2^31 rows),
+ * input or one another), ST_ERR_UNSUPPORTED (more than 16384 channels; 2^31 - 1024
+ * rows or more),
  * ST_ERR_WORKSPACE, ST_ERR_ALIGNMENT, ST_ERR_HIP.
  */
 st_status st_rmsnorm(int64_t rows, int64_t channels, const st_rows* x, const st_rows* residual_or_null,
@@ -843,8 +845,8 @@ st_status st_rmsnorm_backward(int64_t rows, int64_t channels, const st_rows* s, 
 
 /*
  * st_linear - y = act(x w^T + bias) + residual in one pass over the products.
- *   rows, in, out     x is [rows][in], w [out][in], y [rows][out]; rows >= 0, in and
- *                     out >= 1, all below 2^31
+ *   rows, in, out     x is [rows][in], w [out][in], y [rows][out]; rows >= 0 and below
+ *                     2^30, in and out >= 1 and below 2^24
  *   x, w              one type: fp32, bf16, or both in the 8-bit form (inference)
  *   bias_or_null      `out` floats
  *   act               ST_ACT_*
@@ -860,8 +862,9 @@ st_status st_rmsnorm_backward(int64_t rows, int64_t channels, const st_rows* s, 
  * cut the products of eight steps 13 bits below the largest.  Few rows stream the weights once; where tiles are few
  * the products' sum is split over workgroups and joined in a fixed order: the
  * bits depend on sizes and types only.
- * Errors: ST_ERR_WORKSPACE, ST_ERR_ALIGNMENT, ST_ERR_BAD_SHAPE, ST_ERR_UNSUPPORTED (rows of
- * 4 MiB or more), ST_ERR_INVALID_ARG, ST_ERR_HIP.
+ * Errors: ST_ERR_WORKSPACE, ST_ERR_ALIGNMENT, ST_ERR_BAD_SHAPE, ST_ERR_UNSUPPORTED (larger
+ * sizes, rows 4 MiB or more apart, more tiles than one launch holds), ST_ERR_INVALID_ARG,
+ * ST_ERR_HIP.
  */
 size_t st_linear_workspace_bytes(int64_t rows, int64_t in, int64_t out, int32_t type, int32_t backward);
 st_status st_linear(int64_t rows, int64_t in, int64_t out, const st_rows* x, const st_rows* w, const float* bias_or_null,
