@@ -183,31 +183,71 @@ __device__ __forceinline__ uint32_t swap_max(uint32_t v) {
   return max(r[0], r[1]);
 }
 
-// One token's 32 channels (16 in this lane, the others in the lane half across)
-// to an output in bf16 or fp32.
-__device__ __forceinline__ void put_float(const Rows& o, int64_t m, int n0, int cols, int half, const float (&v)[16]) {
-  char* p = o.p + m * o.stride;
+// A block of the epilogue: 32 tokens from m0 on (m0 + lane % 32) by 32 channels from
+// n0 on, of which a lane holds 8 q + 4 half + e in v[4 q + e].  To memory and from it
+// goes 16 bytes a lane, 64 contiguous bytes of a token (four lanes) at a time:
+// swap_rows turns 32 tokens' first and second 32 bytes into 16 tokens' 64 and the
+// other 16's (its own inverse).
+__device__ __forceinline__ void swap_rows(u32x4_t& a, u32x4_t& b) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const u32x2_t t = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane16_swap(a[i], b[i], false, false));
+    a[i] = t[0];
+    b[i] = t[1];
+  }
+}
+struct Spot {
+  int64_t m;                          // of the first 16 tokens' register, of the second m + 16
+  int at;                             // 16-byte piece of the token's 64
+};
+__device__ __forceinline__ Spot spot_of(int64_t m0, int lane) { return {m0 + (lane & 15), (lane >> 4 & 1) * 2 + (lane >> 5)}; }
+
+// NT: outputs that pass the L2s by, larger than they are: operands stay there that
+// are read again (16384 x 2048 x 8192 in bf16 482 -> 439 us, in 8 bits 283 -> 258).
+template <bool NT> __device__ __forceinline__ void put16(char* p, u32x4_t w) {
+  if constexpr (NT) __builtin_nontemporal_store(w, reinterpret_cast<u32x4_any*>(p));
+  else *reinterpret_cast<u32x4_any*>(p) = w;
+}
+
+// A block to an output in bf16 or fp32
+template <bool NT> __device__ __forceinline__ void put_float(const Rows& o, int64_t m0, int n0, int rows, int cols, int lane, const float (&v)[16]) {
   if (n0 + 32 <= cols) {
+    const Spot at = spot_of(m0, lane);
+    char* p = o.p + at.m * o.stride + (int64_t)n0 * (o.type == ST_F32 ? 4 : 2) + at.at * 16;
+    const bool in0 = at.m < rows, in1 = at.m + 16 < rows;
     if (o.type == ST_BF16) {
       // the lanes of one token trade quads: 8 channels in a row each, twice
+      u32x4_t w[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint32_t a0 = pack_bf16(v[8 * j], v[8 * j + 1]), a1 = pack_bf16(v[8 * j + 2], v[8 * j + 3]);
         const uint32_t b0 = pack_bf16(v[8 * j + 4], v[8 * j + 5]), b1 = pack_bf16(v[8 * j + 6], v[8 * j + 7]);
         const u32x2_t lo = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(a0, b0, false, false));
         const u32x2_t hi = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(a1, b1, false, false));
-        *reinterpret_cast<u32x4_any*>(p + (int64_t)(n0 + 16 * j + 8 * half) * 2) = u32x4_t{lo[0], hi[0], lo[1], hi[1]};
+        w[j] = u32x4_t{lo[0], hi[0], lo[1], hi[1]};
       }
+      swap_rows(w[0], w[1]);
+      if (in0) put16<NT>(p, w[0]);
+      if (in1) put16<NT>(p + 16 * o.stride, w[1]);
     } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<f32x4_any*>(p + (int64_t)(n0 + 8 * q + 4 * half) * 4) = f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      for (int j = 0; j < 2; ++j) {
+        u32x4_t w[2];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) w[r / 4][r % 4] = __float_as_uint(v[8 * j + r]);
+        swap_rows(w[0], w[1]);
+        if (in0) put16<NT>(p + 64 * j, w[0]);
+        if (in1) put16<NT>(p + 16 * o.stride + 64 * j, w[1]);
+      }
     }
     return;
   }
+  const int64_t m = m0 + (lane & 31);
+  if (m >= rows) return;
+  char* p = o.p + m * o.stride;
 #pragma unroll
   for (int r = 0; r < 16; ++r) {                        // the last channels
-    const int n = n0 + 8 * (r / 4) + 4 * half + r % 4;
+    const int n = n0 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
     if (n < cols) {
       if (o.type == ST_F32) reinterpret_cast<float*>(p)[n] = v[r];
       else reinterpret_cast<uint16_t*>(p)[n] = (uint16_t)pack_bf16(v[r], 0.f);
@@ -215,9 +255,13 @@ __device__ __forceinline__ void put_float(const Rows& o, int64_t m, int n0, int 
   }
 }
 
-// The same to an output in any type
-__device__ __forceinline__ void put_block(const Rows& o, int64_t m, int n0, int cols, int half, const float (&v)[16]) {
+// The same to an output in any type.
+// (8-bit blocks are 32 bytes of a line, which the L2 joins: past it 16384 x 2048 x 8192
+// took 311 us in place of 263)
+template <bool NT> __device__ __forceinline__ void put_block(const Rows& o, int64_t m0, int n0, int rows, int cols, int lane, const float (&v)[16]) {
   if (o.type == ST_MX8) {
+    const int half = lane >> 5;
+    const int64_t m = m0 + (lane & 31);
     // (channels past the last are zeros here: they have no part in the scale)
     uint32_t top = 0;
 #pragma unroll
@@ -237,12 +281,13 @@ __device__ __forceinline__ void put_block(const Rows& o, int64_t m, int n0, int 
 #pragma unroll
       for (int q = 0; q < 4; ++q) w[q] = mx_codes<true>(v + 4 * q, s);
     }
+    // the lanes of one token trade quads: 16 channels in a row each
+    const u32x2_t a = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false));
+    const u32x2_t b = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false));
+    if (m >= rows) return;
     uint8_t* p = reinterpret_cast<uint8_t*>(o.p) + m * o.stride + n0;
     if (half == 0) o.scales[m * o.scale_stride + (n0 >> 5)] = (uint8_t)s;
     if (n0 + 32 <= cols) {
-      // the lanes of one token trade quads: 16 channels in a row each
-      const u32x2_t a = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false));
-      const u32x2_t b = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false));
       *reinterpret_cast<u32x4_t*>(p + 16 * half) = u32x4_t{a[0], a[1], b[0], b[1]};
     } else {
 #pragma unroll
@@ -253,36 +298,75 @@ __device__ __forceinline__ void put_block(const Rows& o, int64_t m, int n0, int 
     }
     return;
   }
-  put_float(o, m, n0, cols, half, v);
+  put_float<NT>(o, m0, n0, rows, cols, lane, v);
 }
 
-// v = x w^T + bias: pre = v; y = act(v) + residual.  Both lanes of a token come here.
-// PLAIN: v alone, to bf16 or fp32.
-template <bool PLAIN> __device__ __forceinline__ void finish_block(const Finish& f, int64_t m, int n0, int half, float (&v)[16]) {
-  if (m >= f.rows || n0 >= f.cols) return;
-  if constexpr (PLAIN) {
-    put_float(f.y, m, n0, f.cols, half, v);
+// A block of the residual, as it lies: values come out of it when they are added,
+// so that nothing waits for the loads before.
+struct Res { u32x4_t w[4]; };
+__device__ __forceinline__ void load_res(const Rows& o, int64_t m0, int n0, int rows, int cols, int lane, Res& t) {
+  if (n0 + 32 <= cols) {
+    const Spot at = spot_of(m0, lane);
+    // (past the last token: its own again)
+    const char* p = o.p + (int64_t)n0 * (o.type == ST_F32 ? 4 : 2) + at.at * 16;
+    const char* p0 = p + min(at.m, (int64_t)rows - 1) * o.stride;
+    const char* p1 = p + min(at.m + 16, (int64_t)rows - 1) * o.stride;
+    t.w[0] = *reinterpret_cast<const u32x4_any*>(p0);
+    t.w[1] = *reinterpret_cast<const u32x4_any*>(p1);
+    if (o.type == ST_F32) {
+      t.w[2] = *reinterpret_cast<const u32x4_any*>(p0 + 64);
+      t.w[3] = *reinterpret_cast<const u32x4_any*>(p1 + 64);
+    } else {
+      t.w[2] = t.w[3] = u32x4_t{};
+    }
     return;
   }
-  float t[16];
-  if (f.res.type >= 0) {                                // (on its way during the activation)
-    const char* p = f.res.p + m * f.res.stride;
+  const int64_t m = m0 + (lane & 31);
+  const char* p = o.p + m * o.stride;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = n0 + 8 * q + 4 * half;
-      float u[4];
-      load_some<4>(f.res.type, p + (int64_t)n * (f.res.type == ST_F32 ? 4 : 2), f.cols - n, u);
+  for (int r = 0; r < 16; ++r) {                        // the last channels: as values
+    const int n = n0 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
+    float x = 0.f;
+    if (m < rows && n < cols)
+      x = o.type == ST_F32 ? reinterpret_cast<const float*>(p)[n] : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[n] << 16);
+    t.w[r / 4][r % 4] = __float_as_uint(x);
+  }
+}
+__device__ __forceinline__ void add_res(const Rows& o, int n0, int cols, Res& t, float (&v)[16]) {
+  if (n0 + 32 <= cols) {
+    swap_rows(t.w[0], t.w[1]);
+    if (o.type == ST_BF16) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) t[4 * q + i] = u[i];
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {                   // back to quads
+          const u32x2_t u = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(t.w[j][i], t.w[j][2 + i], false, false));
+          v[8 * j + 2 * i] += bf16_lo(u[0]);
+          v[8 * j + 2 * i + 1] += bf16_hi(u[0]);
+          v[8 * j + 4 + 2 * i] += bf16_lo(u[1]);
+          v[8 * j + 4 + 2 * i + 1] += bf16_hi(u[1]);
+        }
+      return;
     }
+    swap_rows(t.w[2], t.w[3]);
   }
-  if (f.pre.type >= 0) put_block(f.pre, m, n0, f.cols, half, v);
-  if (f.act != kActNone) activate(f.act, v);
-  if (f.res.type >= 0) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) v[r] += t[r];
+  for (int r = 0; r < 16; ++r) v[r] += __uint_as_float(t.w[r / 4][r % 4]);
+}
+
+// v = x w^T + bias: pre = v; y = act(v) + residual.  Every lane of the wave comes
+// here; `t`: the block of the residual, if there is one.
+// PLAIN: v alone, to bf16 or fp32.
+template <bool PLAIN, bool NT = false> __device__ __forceinline__ void finish_block(const Finish& f, int64_t m0, int n0, int lane, Res& t, float (&v)[16]) {
+  if (n0 >= f.cols) return;
+  if constexpr (PLAIN) {
+    put_float<NT>(f.y, m0, n0, f.rows, f.cols, lane, v);
+    return;
   }
-  put_block(f.y, m, n0, f.cols, half, v);
+  if (f.pre.type >= 0) put_block<NT>(f.pre, m0, n0, f.rows, f.cols, lane, v);
+  if (f.act != kActNone) activate(f.act, v);
+  if (f.res.type >= 0) add_res(f.res, n0, f.cols, t, v);
+  put_block<NT>(f.y, m0, n0, f.rows, f.cols, lane, v);
 }
 
 // ------------------------------------------------------------- launches

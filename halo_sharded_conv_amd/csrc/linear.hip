@@ -22,6 +22,35 @@ template <int N, int I = 0, class F> __device__ __forceinline__ void static_for(
   }
 }
 
+// 64 lanes' B (16 or 4) bytes from base + offset (past `bytes`: zeros) to LDS, in the order
+// of the lanes.  BYHAND: not by the builtin, whose transfers the compiler waits for before
+// LDS is read again, with every store that it cannot count; the caller waits himself.
+// (An SGPR that a vector instruction wrote is read by the fifth instruction after it at
+// the earliest.)
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+template <int B, bool BYHAND> __device__ __forceinline__ void to_lds(const void* base, int bytes, const void* dst, uint32_t offset, int soffset) {
+#ifdef __HIP_DEVICE_COMPILE__
+  if constexpr (BYHAND) {
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    const i32x4_t r = {(int)(uint32_t)p, (int)(uint32_t)(p >> 32 & 0xFFFF), bytes, 0x00020000};
+    const uint32_t at = (uint32_t)(uintptr_t)(lds_void)dst;
+    int kept;                                           // (the compiler's m0)
+    if constexpr (B == 16)
+      asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
+                   : "=&s"(kept) : "s"(at), "v"(offset), "s"(r), "s"(soffset) : "memory");
+    else
+      asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 4\n\tbuffer_load_dword %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
+                   : "=&s"(kept) : "s"(at), "v"(offset), "s"(r), "s"(soffset) : "memory");
+  } else {
+    static_assert(B == 16, "16 bytes a lane");
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000),
+                                             (lds_void)dst, 16, offset, soffset, 0, 0);
+  }
+#endif
+}
+// Waits for all but the newest N vector memory operations and for LDS
+template <int N> __device__ __forceinline__ void wait_vm() { asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"(N) : "memory"); }
+
 struct GemmArgs {
   Rows a, b;
   Finish f;
@@ -50,8 +79,15 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
   __shared__ __attribute__((aligned(1024))) char b0[OB::BYTES];
   __shared__ __attribute__((aligned(1024))) char b1[OB::BYTES];
   __shared__ __attribute__((aligned(1024))) char sc[2 * SCALES];
+  __shared__ __attribute__((aligned(1024))) float bias[TA];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, wa = wave % WA, wb = wave / WA;
+  // (what depends on it is formed anew for each tile: no registers held meanwhile)
+  auto lane_anew = [&]() __attribute__((always_inline)) -> int {
+    int l = lane;
+    asm("" : "+v"(l));
+    return l;
+  };
 
   // Workgroups go round the 8 XCDs: each XCD takes a run of tiles, eight row tiles
   // deep, so that what its L2 holds is shared; a workgroup takes every so many-th of
@@ -66,8 +102,7 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
   uint32_t offa[QA], offb[QB];
   const char *pa, *pb;
   auto place = [&]() __attribute__((always_inline)) -> void {
-    int l = lane;
-    asm("" : "+v"(l));                                  // (formed anew for each tile: no registers held meanwhile)
+    const int l = lane_anew();
     split = t / tiles;
     const uint32_t u = t - split * tiles, deep = 8, group = deep * g.tiles_a, gi = u / group, first = gi * deep;
     const uint32_t in = u - gi * group, d = min(deep, g.tiles_b - first);
@@ -91,40 +126,41 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
 
   // Stage kt's transfers.  Past the last stage nothing is read: they write zeros.
   const int sta = (int)g.a.stride, stb = (int)g.b.stride;
-  auto fetch = [&](char* as, char* bs, int kt) __attribute__((always_inline)) -> void {
+  auto fetch = [&](auto SWITCH, char* as, char* bs, int kt) __attribute__((always_inline)) -> void {
+    constexpr bool sw = decltype(SWITCH)::value != 0;
     const int left = g.kbytes - kt * 128;               // bytes of the contraction from here on
     const int rows = min(g.k - kt * KT, KT);            // its steps of this stage
     const int na = AC ? rows * sta : min(TA, g.n - n0) * sta, nb = BC ? rows * stb : min(TB, g.m - m0) * stb;
-    const auto ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(AC ? pa + (int64_t)kt * KT * sta : pa), (short)0,
-                                                      kt < k_hi ? na : 0, 0x00020000);
-    const auto rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(BC ? pb + (int64_t)kt * KT * stb : pb), (short)0,
-                                                      kt < k_hi ? nb : 0, 0x00020000);
+    const char* ba = AC ? pa + (int64_t)kt * KT * sta : pa;
+    const char* bb = BC ? pb + (int64_t)kt * KT * stb : pb;
     // (kPastEnd stays past every end with the rows added)
     static_assert((AC || OA::ALIKE) && (BC || OB::ALIKE), "one byte offset for all transfers along the contraction");
     const uint32_t a_first = !AC && OA::dma_byte(wave, lane, 0) >= left ? kPastEnd : offa[0];
     const uint32_t b_first = !BC && OB::dma_byte(wave, lane, 0) >= left ? kPastEnd : offb[0];
 #pragma unroll
     for (int i = 0; i < OA::NI; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void)OA::dma_dst(as, wave, i), 16,
-                                               OA::ALIKE ? a_first + (uint32_t)(i * OA::ROWS_ON * sta) : offa[i % QA], AC ? 0 : kt * 128, 0, 0);
+      to_lds<16, sw>(ba, kt < k_hi ? na : 0, OA::dma_dst(as, wave, i), OA::ALIKE ? a_first + (uint32_t)(i * OA::ROWS_ON * sta) : offa[i % QA], AC ? 0 : kt * 128);
 #pragma unroll
     for (int i = 0; i < OB::NI; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void)OB::dma_dst(bs, wave, i), 16,
-                                               OB::ALIKE ? b_first + (uint32_t)(i * OB::ROWS_ON * stb) : offb[i % QB], BC ? 0 : kt * 128, 0, 0);
+      to_lds<16, sw>(bb, kt < k_hi ? nb : 0, OB::dma_dst(bs, wave, i), OB::ALIKE ? b_first + (uint32_t)(i * OB::ROWS_ON * stb) : offb[i % QB], BC ? 0 : kt * 128);
   };
   // 8-bit operands: the scale bytes of stages kt .. kt + 3, 16 of every row (a row's
   // may end before; the bytes past it are not used)
-  auto fetch_scales = [&](int kt) __attribute__((always_inline)) -> void {
+  auto fetch_scales = [&](auto SWITCH, int kt) __attribute__((always_inline)) -> void {
     if constexpr (MX) {
       if (wave < (TA + TB) / 64) {
         const bool of_a = wave < TA / 64;
         const Rows& o = of_a ? g.a : g.b;
         const int row0 = of_a ? n0 : m0, rows = of_a ? min(TA, g.n - n0) : min(TB, g.m - m0), first = of_a ? wave * 64 : wave * 64 - TA;
-        const auto rs = __builtin_amdgcn_make_buffer_rsrc(o.scales + (int64_t)row0 * o.scale_stride, (short)0,
-                                                          kt < k_hi ? rows * (int)o.scale_stride : 0, 0x00020000);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void)(sc + ((kt - k_lo) >> 2 & 1) * SCALES + wave * 1024), 16,
-                                                 (uint32_t)((first + lane) * (int)o.scale_stride), kt * 4, 0, 0);
+        to_lds<16, decltype(SWITCH)::value != 0>(o.scales + (int64_t)row0 * o.scale_stride, kt < k_hi ? rows * (int)o.scale_stride : 0,
+                                                 sc + ((kt - k_lo) >> 2 & 1) * SCALES + wave * 1024, (uint32_t)((first + lane_anew()) * (int)o.scale_stride), kt * 4);
       }
+    }
+  };
+  // The tile's bias (the first split's; zeros past the last channel)
+  auto fetch_bias = [&]() __attribute__((always_inline)) -> void {
+    if (wave < TA / 64) {
+      to_lds<4, true>(g.f.bias, g.f.bias && split == 0 ? g.n * 4 : 0, bias + wave * 64, (uint32_t)(n0 + wave * 64 + lane_anew()) * 4, 0);
     }
   };
 
@@ -187,16 +223,24 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
     }
     __builtin_amdgcn_sched_barrier(0);
   };
+  // Transfers and stores end in the order in which they set out, so waiting for all
+  // but the newest `STORES` of a whole tile, which has at least that many, waits for the next
+  // tile's transfers and not for the stores behind them.  They have until the end of the
+  // second stage, whose transfers set out after them (8-bit 16384 x 2048 x 8192: 313 -> 285 us).
+  constexpr int STORES = 2 * NA * NB;
+  bool behind = false;
+
   // Stage kt in (as, bs), stage kt + 1 on its way to (an, bn).  Fragments are read one
   // step ahead of the products; before the last step's products every wave has read
   // all of stage kt, so the workgroup meets there, stage kt + 2 sets out into the
   // buffers of stage kt, and the first fragments of stage kt + 1 are on their way
   // while the matrix cores still have a step to do.
-  auto stage = [&](auto CUR, char* as, char* bs, const char* an, const char* bn, int kt) __attribute__((always_inline)) -> void {
+  // FIRST: of a tile.
+  auto stage = [&](auto CUR, auto FIRST, char* as, char* bs, const char* an, const char* bn, int kt) __attribute__((always_inline)) -> void {
     constexpr int cur = decltype(CUR)::value;
     // (its buffer's last readers are two meetings back, its first three ahead)
     if constexpr (MX && cur == 0) {
-      if ((kt - k_lo & 3) == 0) fetch_scales(kt + 4);
+      if ((kt - k_lo & 3) == 0) fetch_scales(Int<0>{}, kt + 4);
     }
     static_for<STEPS>([&](auto S) __attribute__((always_inline)) -> void {
       constexpr int s = decltype(S)::value;
@@ -205,11 +249,12 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
         read(Int<(s + 1) & 1>{}, Int<s + 1>{}, Int<cur>{}, as, bs);
       } else {
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0070);
+        if (decltype(FIRST)::value && behind) wait_vm<STORES>();
+        else __builtin_amdgcn_s_waitcnt(0x0070);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         read(Int<0>{}, Int<0>{}, Int<1 - cur>{}, an, bn);
-        fetch(as, bs, kt + 2);
+        fetch(Int<0>{}, as, bs, kt + 2);
       }
       multiply(Int<s & 1>{}, Int<s>{}, Int<cur>{});
       order(Int<MX && s == 0 ? NA + NB : 0>{});
@@ -220,67 +265,85 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
   // a tile's epilogue.  (Their buffers' last readers are behind the last meeting; what
   // is read after it is not used.)
   place();
-  fetch_scales(k_lo);
-  fetch(a0, b0, k_lo);
-  fetch(a1, b1, k_lo + 1);
+  fetch_scales(Int<1>{}, k_lo);
+  fetch_bias();
+  fetch(Int<1>{}, a0, b0, k_lo);
+  fetch(Int<1>{}, a1, b1, k_lo + 1);
   for (;;) {
-    // the sums start from the bias (the first split's do; zeros past the last channel)
-    {
-      const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(g.f.bias), (short)0, g.f.bias && split == 0 ? g.n * 4 : 0, 0x00020000);
-#pragma unroll
-      for (int i = 0; i < NA; ++i) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x4_t t = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (n0 + wa * PA + 32 * i + 8 * q + 4 * half) * 4, 0, 0));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][0][4 * q + e] = t[e];
-        }
-#pragma unroll
-        for (int j = 1; j < NB; ++j) acc[i][j] = acc[i][0];
-      }
-    }
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070);
+    if (behind) wait_vm<STORES + OA::NI + OB::NI>();
+    else wait_vm<0>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    // the sums start from the bias
+    const int bias_at = wa * PA + (lane_anew() >> 5) * 4;
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 t = *reinterpret_cast<const float4*>(bias + bias_at + 32 * i + 8 * q);
+        acc[i][0][4 * q] = t.x; acc[i][0][4 * q + 1] = t.y; acc[i][0][4 * q + 2] = t.z; acc[i][0][4 * q + 3] = t.w;
+      }
+#pragma unroll
+      for (int j = 1; j < NB; ++j) acc[i][j] = acc[i][0];
+    }
     read_scales(Int<0>{}, k_lo);
     read(Int<0>{}, Int<0>{}, Int<0>{}, a0, b0);
     int kt = k_lo;
-    for (; kt + 2 <= k_hi; kt += 2) {
-      stage(Int<0>{}, a0, b0, a1, b1, kt);
-      stage(Int<1>{}, a1, b1, a0, b0, kt + 1);
+    if (!MX && kt + 2 <= k_hi) {                        // (8-bit operands: no registers for a second copy)
+      stage(Int<0>{}, Int<1>{}, a0, b0, a1, b1, kt);
+      stage(Int<1>{}, Int<0>{}, a1, b1, a0, b0, kt + 1);
+      kt += 2;
     }
-    if (kt < k_hi) stage(Int<0>{}, a0, b0, a1, b1, kt);
+    for (; kt + 2 <= k_hi; kt += 2) {
+      stage(Int<0>{}, Int<0>{}, a0, b0, a1, b1, kt);
+      stage(Int<1>{}, Int<0>{}, a1, b1, a0, b0, kt + 1);
+    }
+    if (kt < k_hi) stage(Int<0>{}, Int<0>{}, a0, b0, a1, b1, kt);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0x0070);                 // (no transfer of this tile meets one of the next)
     asm volatile("" ::: "memory");
-    const int em = m0, en = n0, es = split;
+    const int em = m0 + wb * PB, en = n0 + wa * PA, es = split;
+    const bool added = !PLAIN && g.f.res.type >= 0;
+    constexpr bool AHEAD = !MX;                         // (8-bit operands: no registers for it)
+    Res res[2];                                         // the block's, the next one's
+    behind = m0 + TB <= g.m && n0 + TA <= g.n;
     t += t_step;
     const bool more = t < t_end;
     if (more) {
       place();
-      fetch_scales(k_lo);
-      fetch(a0, b0, k_lo);
-      fetch(a1, b1, k_lo + 1);
+      fetch_scales(Int<1>{}, k_lo);
+      fetch_bias();
+      fetch(Int<1>{}, a0, b0, k_lo);
+      fetch(Int<1>{}, a1, b1, k_lo + 1);
     }
-    int l = lane;
-    asm("" : "+v"(l));
+    asm volatile("" ::: "memory");
+    int l = lane_anew();
+    if (AHEAD && added) load_res(g.f.res, em, en, g.f.rows, g.f.cols, l, res[0]);
     static_for<NA * NB>([&](auto U) __attribute__((always_inline)) -> void {
       constexpr int i = decltype(U)::value / NB, j = decltype(U)::value % NB;
-      const int64_t m = em + wb * PB + 32 * j + (l & 31);
-      const int n = en + wa * PA + 32 * i;
+      constexpr int u = decltype(U)::value, in = (u + 1) / NB, jn = (u + 1) % NB;
+      const int64_t m = em + 32 * j;
+      const int n = en + 32 * i;
+      if constexpr (!AHEAD) {
+        l = lane_anew();
+        res[0] = Res{};
+        if (added) load_res(g.f.res, m, n, g.f.rows, g.f.cols, l, res[0]);
+      } else if constexpr (u + 1 < NA * NB) {
+        if (added) load_res(g.f.res, em + 32 * jn, en + 32 * in, g.f.rows, g.f.cols, l, res[(u + 1) & 1]);
+      }
       float v[16];
 #pragma unroll
       for (int r = 0; r < 16; ++r) v[r] = acc[i][j][r];
       if (PLAIN && g.part) {
-        if (m < g.m && n < g.n) {
-          float* p = g.part + ((int64_t)es * g.m + m) * g.ld + n + 4 * (l >> 5);
+        if (m + (l & 31) < g.m && n < g.n) {
+          float* p = g.part + ((int64_t)es * g.m + m + (l & 31)) * g.ld + n + 4 * (l >> 5);
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             *reinterpret_cast<f32x4_t*>(p + 8 * q) = f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
         }
       } else {
-        finish_block<PLAIN>(g.f, m, n, l >> 5, v);
+        finish_block<PLAIN, TA == 256>(g.f, m, n, l, res[AHEAD ? u & 1 : 0], v);
       }
     });
     if (!more) break;
@@ -290,11 +353,13 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
 
 // Adds the splits' partial sums in order and finishes the blocks, a wave and a
 // workgroup each.  Four splits are on their way at once: with few blocks the pass
-// is as long as its loads are late (33 x 2048 in 4 splits: 5.7 -> 4.1 us us).
+// is as long as its loads are late (33 x 2048 in 4 splits: 5.7 -> 4.1 us).
 __global__ __launch_bounds__(64) void gemm_join(const float* __restrict__ part, int splits, int64_t ld, Finish f, int blocks_n) {
   const int lane = threadIdx.x & 63, half = lane >> 5;
-  const int64_t m = (int64_t)(blockIdx.x / blocks_n) * 32 + (lane & 31);
+  const int64_t m0 = (int64_t)(blockIdx.x / blocks_n) * 32, m = m0 + (lane & 31);
   const int n0 = (int)(blockIdx.x % blocks_n) * 32;
+  Res t;
+  if (f.res.type >= 0) load_res(f.res, m0, n0, f.rows, f.cols, lane, t);
   float v[16];
 #pragma unroll
   for (int r = 0; r < 16; ++r) v[r] = 0.f;
@@ -321,7 +386,7 @@ __global__ __launch_bounds__(64) void gemm_join(const float* __restrict__ part, 
       for (int r = 0; r < 16; ++r) v[r] += t[r / 4][r % 4];
     }
   }
-  finish_block<false>(f, m, n0, half, v);
+  finish_block<false>(f, m0, n0, lane, t, v);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -437,7 +502,9 @@ template <class T, int MB> __global__ __launch_bounds__(64 * kFewWaves, 2) void 
     }
   }
   if (!g.part) {
-    finish_block<false>(g.f, m, n0, half, v);
+    Res t;
+    if (g.f.res.type >= 0) load_res(g.f.res, 32 * wave, n0, g.f.rows, g.f.cols, lane, t);
+    finish_block<false>(g.f, 32 * wave, n0, lane, t, v);
   } else if (m < g.m) {
     float* p = g.part + ((int64_t)split * g.m + m) * g.ld + n0 + 4 * half;
 #pragma unroll
