@@ -7,6 +7,12 @@
 // One kernel for all three: an operand whose contraction is not contiguous lies in
 // LDS as it lies in memory and is read by the transposing LDS read, so nothing is
 // transposed in memory.
+//
+// Bound: the matrix cores; 256 x 256 tiles read each operand's stage (32 KB) once for
+// 8 MFLOP.  16384 x 8192 x 2048 in bf16 419 us (1313 TFLOP/s), in 8 bits 238 (2308); 16384 x
+// 2048 x 8192 475 us (1156: eight tiles a compute unit, whose stores of 128 KB each
+// are partly waited for); dw of it 438 us (1257).  Up to 64 rows: the weights' bytes
+// (1 x 2048 x 8192 in bf16 9.6 us, 3.5 TB/s).
 #include <cmath>
 
 #include "linear.h"
