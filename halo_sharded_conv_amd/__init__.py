@@ -976,6 +976,19 @@ def _act(act: str, what: str) -> int:
     return _ACTS[act]
 
 
+def _floats(t, what: str, min_bytes: int, device: int):
+    """Floats of the current device, or None."""
+    if t is not None and not (getattr(t, "is_cuda", False) and t.get_device() == device):
+        _here(t, what, device)
+    return _typed(t, what, _FP32, min_bytes)
+
+
+def _ws_here(workspace, device: int):
+    if workspace is not None:
+        _here(workspace, "workspace", device)
+    return _ws(workspace)
+
+
 def st_mx8_store(x, out: Mx8, stream=None) -> None:
     """x: [rows, channels], float32 or bfloat16, into the 8-bit form."""
     dev = _device()
@@ -1000,9 +1013,9 @@ def st_rmsnorm(x, residual, gamma, eps: float, total=None, y=None, y8: Optional[
     dev = _device()
     n, c = _shape(x, "st_rmsnorm x")
     _check(lib.st_rmsnorm(n, c, _rows(x, "st_rmsnorm", "x", n, c, dev), _rows(residual, "st_rmsnorm", "residual", n, c, dev),
-                          _typed(gamma, "gamma", _FP32, 4 * c), float(eps), _rows(total, "st_rmsnorm", "total", n, c, dev),
+                          _floats(gamma, "gamma", 4 * c, dev), float(eps), _rows(total, "st_rmsnorm", "total", n, c, dev),
                           _rows(y, "st_rmsnorm", "y", n, c, dev), _rows(y8, "st_rmsnorm", "y8", n, c, dev),
-                          _typed(rstd, "rstd", _FP32, 4 * n), _stream(stream)), what)
+                          _floats(rstd, "rstd", 4 * n, dev), _stream(stream)), what)
 
 
 def st_rmsnorm_backward_workspace_bytes(rows: int, channels: int) -> int:
@@ -1015,11 +1028,11 @@ def st_rmsnorm_backward(s, dy, dtotal, gamma, rstd, dx, dgamma, workspace, strea
     what = "st_rmsnorm_backward"
     dev = _device()
     n, c = _shape(s, "st_rmsnorm_backward s")
-    ws, nb = _ws(workspace)
+    ws, nb = _ws_here(workspace, dev)
     _check(lib.st_rmsnorm_backward(n, c, _rows(s, "st_rmsnorm_backward", "s", n, c, dev), _rows(dy, "st_rmsnorm_backward", "dy", n, c, dev),
-                                   _rows(dtotal, "st_rmsnorm_backward", "dtotal", n, c, dev), _typed(gamma, "gamma", _FP32, 4 * c),
-                                   _typed(rstd, "rstd", _FP32, 4 * n), _rows(dx, "st_rmsnorm_backward", "dx", n, c, dev),
-                                   _typed(dgamma, "dgamma", _FP32, 4 * c), ws, nb, _stream(stream)), what)
+                                   _rows(dtotal, "st_rmsnorm_backward", "dtotal", n, c, dev), _floats(gamma, "gamma", 4 * c, dev),
+                                   _floats(rstd, "rstd", 4 * n, dev), _rows(dx, "st_rmsnorm_backward", "dx", n, c, dev),
+                                   _floats(dgamma, "dgamma", 4 * c, dev), ws, nb, _stream(stream)), what)
 
 
 def st_linear_workspace_bytes(rows: int, channels_in: int, channels_out: int, dtype, backward: bool = False) -> int:
@@ -1035,9 +1048,9 @@ def st_linear(x, w, bias, y, act: str = "none", residual=None, pre=None, workspa
     dev = _device()
     n, k = _shape(x, "st_linear x")
     m = _shape(w, "st_linear w")[0]
-    ws, nb = _ws(workspace)
+    ws, nb = _ws_here(workspace, dev)
     _check(lib.st_linear(n, k, m, _rows(x, "st_linear", "x", n, k, dev), _rows(w, "st_linear", "w", m, k, dev),
-                         _typed(bias, "bias", _FP32, 4 * m), _act(act, what), _rows(residual, "st_linear", "residual", n, m, dev),
+                         _floats(bias, "bias", 4 * m, dev), _act(act, what), _rows(residual, "st_linear", "residual", n, m, dev),
                          _rows(y, "st_linear", "y", n, m, dev), _rows(pre, "st_linear", "pre", n, m, dev), ws, nb, _stream(stream)), what)
 
 
@@ -1048,9 +1061,9 @@ def st_linear_backward(x, w, dy, dx, dw, dbias, act: str = "none", pre=None, wor
     dev = _device()
     n, k = _shape(x, "st_linear_backward x")
     m = _shape(w, "st_linear_backward w")[0]
-    ws, nb = _ws(workspace)
+    ws, nb = _ws_here(workspace, dev)
     _check(lib.st_linear_backward(n, k, m, _rows(x, "st_linear_backward", "x", n, k, dev), _rows(w, "st_linear_backward", "w", m, k, dev),
                                   _act(act, what), _rows(pre, "st_linear_backward", "pre", n, m, dev),
                                   _rows(dy, "st_linear_backward", "dy", n, m, dev), _rows(dx, "st_linear_backward", "dx", n, k, dev),
-                                  _rows(dw, "st_linear_backward", "dw", m, k, dev), _typed(dbias, "dbias", _FP32, 4 * m), ws, nb,
+                                  _rows(dw, "st_linear_backward", "dw", m, k, dev), _floats(dbias, "dbias", 4 * m, dev), ws, nb,
                                   _stream(stream)), what)

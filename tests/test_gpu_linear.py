@@ -297,3 +297,75 @@ def test_same_bits_twice(gpu_lib):
         got.append((dx, dw, db))
     for a, b, c in zip(*got):
         assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "mx8"])
+@pytest.mark.parametrize("k", [40, 64, 136, 200, 520, 1000])
+@pytest.mark.parametrize("y,pre,res", [("bf16", "", ""), ("f32", "", ""), ("bf16", "mx8", "f32"), ("mx8", "", "bf16"), ("f32", "bf16", "f32")])
+def test_many_tiles_of_whole_numbers(gpu_lib, dtype, k, y, pre, res):
+    """Several tiles a workgroup, whole ones and ragged ones, of one stage and more,
+    bit for bit: whole numbers up to 3, whose sums (below 9 * 1000 + 3 + 3) are exact in fp32
+    and in the 8-bit instructions (products of up to 4 bits, sums of eight in 7)."""
+    say(f"linear whole numbers k {k} {dtype} y {y} pre {pre} res {res}")
+    m, n = 10247, 2312
+    gen = torch.Generator(device="cuda").manual_seed(k)
+    draw = lambda *s: torch.randint(-3, 4, s, generator=gen, device="cuda").float()  # noqa: E731
+    xf, wf, b, r = draw(m, k), draw(n, k), draw(n), draw(m, n)
+
+    def held(t, d):
+        if d == "mx8":
+            o = gpu_lib.mx8_empty(*t.shape)
+            gpu_lib.st_mx8_store(t, o)
+            return o
+        return t.to(TORCH[d])
+
+    def blank(d):
+        return None if not d else gpu_lib.mx8_empty(m, n) if d == "mx8" else torch.full((m, n), 99.0, device="cuda").to(TORCH[d])
+
+    yo, po = blank(y), blank(pre)
+    ws = torch.empty(max(16, gpu_lib.st_linear_workspace_bytes(m, k, n, dtype)), dtype=torch.uint8, device="cuda")
+    gpu_lib.st_linear(held(xf, dtype), held(wf, dtype), b, yo, act="relu", residual=held(r, res) if res else None, pre=po, workspace=ws)
+    z = (xf.double() @ wf.double().t() + b.double()).float()
+    want = torch.relu(z) + (r if res else 0)
+    for got, value, d in ((yo, want, y), (po, z, pre)):
+        if d == "mx8":
+            exact = held(value, "mx8")
+            blocks = -(-n // 32)
+            assert torch.equal(got.codes[:, :n], exact.codes[:, :n]) and torch.equal(got.scales[:, :blocks], exact.scales[:, :blocks])
+        elif d:
+            assert torch.equal(got, value.to(TORCH[d]))
+
+
+def test_two_graphs_of_one_workspace(gpu_lib):
+    """Captured calls that share a workspace, replayed in turns with eager work between."""
+    m, k, n = 96, 4104, 264                               # split and joined, rows copied whole
+    rng = np.random.default_rng(13)
+    x = [torch.from_numpy(rng.normal(size=(m, k))).bfloat16().cuda() for _ in range(2)]
+    w = torch.from_numpy(rng.normal(size=(n, k)) / 64).bfloat16().cuda()
+    dy = torch.from_numpy(rng.normal(size=(m, n))).bfloat16().cuda()
+    need = max(gpu_lib.st_linear_workspace_bytes(m, k, n, "bf16"), gpu_lib.st_linear_workspace_bytes(m, k, n, "bf16", backward=True))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def outputs():
+        return [torch.zeros(m, n, device="cuda"), torch.zeros(m, k, device="cuda"), torch.zeros(n, k, device="cuda"), torch.zeros(n, device="cuda")]
+
+    def run(i, o):
+        gpu_lib.st_linear(x[i], w, None, o[0], act="silu", workspace=ws)
+        gpu_lib.st_linear_backward(x[i], w, dy, *o[1:], workspace=ws)
+
+    want, outs, graphs = [outputs() for _ in range(2)], [outputs() for _ in range(2)], []
+    for i in range(2):
+        run(i, want[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            run(i, outs[i])
+    for turn in range(3):
+        for i in range(2):
+            for t in outs[i]:
+                t.zero_()
+            ws.fill_(0xFF)
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(outs[i], want[i])), f"turn {turn} graph {i}"

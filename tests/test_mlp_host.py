@@ -122,3 +122,18 @@ def test_binding_checks():
     e = hsc.mx8_empty(3, 33, device="cpu")
     assert e.codes.shape == (3, 48) and e.scales.shape == (3, 4) and e.rows == 3
     assert hsc._rows(None, "call", "x", 4, 4, 0) is None
+
+
+def test_vectors_of_another_device():
+    """Vectors and workspaces beside a call's rows are of the current device too."""
+    class Elsewhere:
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+
+    for check in (lambda: hsc._floats(Elsewhere(), "bias", 4, 0), lambda: hsc._ws_here(Elsewhere(), 0),
+                  lambda: hsc._floats(torch.zeros(4), "bias", 16, 0), lambda: hsc._ws_here(torch.zeros(4), 0)):
+        with pytest.raises(hsc.ShardConvError):
+            check()
+    assert not hsc._floats(None, "bias", 4, 0) and hsc._ws_here(None, 0)[1] == 0
