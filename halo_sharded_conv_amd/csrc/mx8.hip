@@ -4,8 +4,12 @@
 // Bound: HBM; a pass reads every value once and writes it once (1 + 1/32 bytes
 // for the 8-bit side).  A lane holds 8 channels, so that four lanes hold a block
 // and its largest magnitude crosses them by two DPP steps; a code row is written
-// 8 bytes a lane, a block's scale by its first lane.  2048^2 x 64 in bf16: stored in
-// 173 us (4.7 TB/s), read back in 150 (5.4).
+// 8 bytes a lane, a block's scale by its first lane.  Both write past the caches:
+// 16384 x 8192 in bf16 stored in 63 us in place of 76 (6.4 TB/s), read back in 58 in
+// place of 80 (7.0), and a product of 16384 x 2048 x 8192 that writes into what has just been
+// read back does not wait for it (the two 698 -> 605 us); reading back codes just
+// stored (134 MB, which the last cache holds) takes 10 us longer.  2048^2 x 64 in bf16:
+// 147 us (5.5 TB/s) and 157.
 #include <algorithm>
 #include <string>
 
@@ -52,7 +56,7 @@ template <class T> __global__ __launch_bounds__(kMxThreads) void mx8_store(const
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = max(top, mx_bits(v[i][j]));
     const int s = mx_scale(block_max<8>(top));
-    store_codes<8>(a.out, g.row, g.c, g.n, v[i], s);
+    store_codes<8, true>(a.out, g.row, g.c, g.n, v[i], s);
   }
 }
 
@@ -72,7 +76,7 @@ template <bool ACT> __global__ __launch_bounds__(kMxThreads) void mx8_load(const
     mx_values(w[i][0], s[i], v);
     mx_values(w[i][1], s[i], v + 4);
     if constexpr (ACT) activate(a.act, v);
-    if (g.n > 0) store_some<8>(a.out.type, a.out.p + (int64_t)g.row * a.out.stride + (int64_t)g.c * (a.out.type == ST_F32 ? 4 : 2), g.n, v);
+    if (g.n > 0) store_some<8, true>(a.out.type, a.out.p + (int64_t)g.row * a.out.stride + (int64_t)g.c * (a.out.type == ST_F32 ? 4 : 2), g.n, v);
   }
 }
 

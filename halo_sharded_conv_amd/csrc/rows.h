@@ -253,14 +253,15 @@ template <int VEC> __device__ __forceinline__ uint32_t block_max(uint32_t v) {
 
 // VEC channels' codes of scale byte s at (row, c), of which n exist; the group that
 // starts a block writes its scale.  Codes past the row's end are left as they are.
-template <int VEC> __device__ __forceinline__ void store_codes(const Rows& o, int64_t row, int c, int n, const float (&v)[VEC], int s) {
+template <int VEC, bool NT = false> __device__ __forceinline__ void store_codes(const Rows& o, int64_t row, int c, int n, const float (&v)[VEC], int s) {
   if (n <= 0) return;
   uint8_t* p = reinterpret_cast<uint8_t*>(o.p) + row * o.stride + c;
   uint32_t w[VEC / 4];
 #pragma unroll
   for (int i = 0; i < VEC / 4; ++i) w[i] = mx_codes<true>(v + 4 * i, s);
   if (n >= VEC) {
-    if constexpr (VEC == 8) *reinterpret_cast<u32x2_t*>(p) = u32x2_t{w[0], w[1]};
+    if constexpr (VEC == 8 && NT) __builtin_nontemporal_store(u32x2_t{w[0], w[1]}, reinterpret_cast<u32x2_t*>(p));
+    else if constexpr (VEC == 8) *reinterpret_cast<u32x2_t*>(p) = u32x2_t{w[0], w[1]};
     else *reinterpret_cast<uint32_t*>(p) = w[0];
   } else {
 #pragma unroll
