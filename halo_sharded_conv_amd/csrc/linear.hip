@@ -548,7 +548,7 @@ constexpr Pace kPace[2][3] = {{{1.0, 1.45, 7.0}, {0.48, 0.33, 3.0}, {0.42, 0.22,
 
 // Tile shape and split of the contraction: the least time of the fullest compute
 // unit, with the partial sums' way through memory (7 TB/s, 5 us for the join).
-// exact: 8-bit operands with an fp32 output, which the middle tile alone has.  cols:
+// exact: 8-bit operands with an output that is no bf16, which the middle tile alone has.  cols:
 // the weights are read across their rows.
 Choice choose(int64_t m, int64_t n, int64_t k, int type, bool exact, bool cols) {
   const int kt = 128 / type_size(type);
@@ -628,7 +628,9 @@ size_t product_bytes(int64_t m, int64_t n, int64_t k, int type, bool cols) {
 
 st_status product_launch(const Product& p, void* workspace, hipStream_t st) {
   if (p.k == 0) return join_launch(nullptr, 0, p.f, st);       // an empty sum: the epilogue of zeros
-  const bool exact = p.type == ST_MX8 && (p.f.y.type == ST_F32 || p.f.pre.type == ST_F32);
+  // (an 8-bit output too: a cut sum lands on a code's other side now and then, 6% off,
+  // 0.001 of the norm where the exact sums' codes are those of the 64-bit values)
+  const bool exact = p.type == ST_MX8 && (p.f.y.type != ST_BF16 || (p.f.pre.type >= 0 && p.f.pre.type != ST_BF16));
   const Choice c = choose(p.m, p.n, p.k, p.type, exact, p.a_col);
   const bool few = c.shape == kFewShape;
   const Shape h = few ? Shape{32, kFewRows, 1} : shape_of(p.type, c.shape);
