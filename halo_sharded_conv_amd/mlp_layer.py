@@ -17,7 +17,9 @@ and 32-bit buffers of the forward steps are scratch then, which the layers of
 one model may share (`scratch`).
 
 products="mx8" (forward only) multiplies in 8 bits: weights rounded once, the
-norm's and the activation's outputs rounded where they are written.
+norm's output where it is written, the hidden values in a pass of their own (from
+bf16: an 8-bit output of an 8-bit product would widen its operands, 128^2 cells of 2048 to
+8192 channels 1608 us, so 844).
 
 torch is used for allocation and views only.
 """
@@ -82,9 +84,10 @@ class ShardedMLP:
             self.w_up, self.w_down = mx8_empty(hidden, channels, device), mx8_empty(channels, hidden, device)
             if scratch is None:
                 self.total, self.normed8, self.h8 = new(t, channels), mx8_empty(t, channels, device), mx8_empty(t, hidden, device)
-                self.y = new(t, channels, dt=bf16)
+                self.y, self.h = new(t, channels, dt=bf16), new(t, hidden, dt=bf16)
             else:
                 self.total, self.normed8, self.h8, self.y = scratch.total, scratch.normed8, scratch.h8, scratch.y
+                self.h = scratch.h
         else:
             self.w_up, self.w_down = new(hidden, channels, dt=bf16), new(channels, hidden, dt=bf16)
             if scratch is None:
@@ -139,7 +142,8 @@ class ShardedMLP:
         branch)) (self.y, written by the next call again)."""
         if self.products == "mx8":
             st_rmsnorm(x, branch, self.gamma, self.eps, total=self.total, y8=self.normed8, stream=stream)
-            st_linear(self.normed8, self.w_up, self.b_up, self.h8, act=self.act, workspace=self.ws, stream=stream)
+            st_linear(self.normed8, self.w_up, self.b_up, self.h, act=self.act, workspace=self.ws, stream=stream)
+            st_mx8_store(self.h, self.h8, stream)
             st_linear(self.h8, self.w_down, self.b_down, self.y, residual=self.total, workspace=self.ws, stream=stream)
             return self.y
         eight = self.kept == "mx8"
