@@ -16,6 +16,7 @@
 #include <cmath>
 
 #include "linear.h"
+#include "linear_plan.h"
 
 namespace st {
 namespace {
@@ -151,15 +152,17 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
       to_lds<16, sw>(bb, kt < k_hi ? nb : 0, OB::dma_dst(bs, wave, i), OB::ALIKE ? b_first + (uint32_t)(i * OB::ROWS_ON * stb) : offb[i % QB], BC ? 0 : kt * 128);
   };
   // 8-bit operands: the scale bytes of stages kt .. kt + 3, 16 of every row (a row's
-  // may end before; the bytes past it are not used)
+  // may end before; the bytes past it are not used, and none past the last row's are read)
   auto fetch_scales = [&](auto SWITCH, int kt) __attribute__((always_inline)) -> void {
     if constexpr (MX) {
       if (wave < (TA + TB) / 64) {
-        const bool of_a = wave < TA / 64;
+        int w = wave;
+        asm("" : "+s"(w));                              // (formed anew: no scalar registers held from stage to stage)
+        const bool of_a = w < TA / 64;
         const Rows& o = of_a ? g.a : g.b;
-        const int row0 = of_a ? n0 : m0, rows = of_a ? min(TA, g.n - n0) : min(TB, g.m - m0), first = of_a ? wave * 64 : wave * 64 - TA;
-        to_lds<16, decltype(SWITCH)::value != 0>(o.scales + (int64_t)row0 * o.scale_stride, kt < k_hi ? rows * (int)o.scale_stride : 0,
-                                                 sc + ((kt - k_lo) >> 2 & 1) * SCALES + wave * 1024, (uint32_t)((first + lane_anew()) * (int)o.scale_stride), kt * 4);
+        const int row0 = of_a ? n0 : m0, rows = of_a ? min(TA, g.n - n0) : min(TB, g.m - m0), first = of_a ? w * 64 : w * 64 - TA;
+        to_lds<16, decltype(SWITCH)::value != 0>(o.scales + (int64_t)row0 * o.scale_stride, kt < k_hi ? scale_span(rows, (int)o.scale_stride, g.blocks_k) : 0,
+                                                 sc + ((kt - k_lo) >> 2 & 1) * SCALES + wave * 1024, (uint32_t)((first + lane_anew()) * (int)o.scale_stride + kt * 4), 0);
       }
     }
   };
