@@ -16,8 +16,9 @@ channels bytes a channel and cell in place of 6 + 4 hidden / channels.  The 16-
 and 32-bit buffers of the forward steps are scratch then, which the layers of
 one model may share (`scratch`).
 
-products="mx8" (forward only) multiplies in 8 bits: weights rounded once, the
-norm's output where it is written, the hidden values in a pass of their own (from
+products="mx8" (forward only: nothing is kept, so that every buffer of the steps is
+scratch, whatever `kept` says) multiplies in 8 bits: weights rounded once, the norm's
+output where it is written, the hidden values in a pass of their own (from
 bf16: an 8-bit output of an 8-bit product would widen its operands, 128^2 cells of 2048 to
 8192 channels 1608 us, so 844).
 
@@ -67,10 +68,12 @@ class ShardedMLP:
             cells = [a * b for a in cells for b in s]
         self.starts = [sum(cells[:i]) for i in range(len(cells) + 1)]
         self.tokens = t = self.starts[-1]
-        if scratch is not None and (scratch.tokens, scratch.channels, scratch.hidden, scratch.kept, scratch.products) != \
-                (t, channels, hidden, kept, products):
+        # (8-bit products keep nothing: all their buffers are scratch)
+        held = lambda k, p: None if p == "mx8" else k  # noqa: E731
+        if scratch is not None and (scratch.tokens, scratch.channels, scratch.hidden, scratch.products, held(scratch.kept, scratch.products)) != \
+                (t, channels, hidden, products, held(kept, products)):
             raise ShardConvError(2, "ShardedMLP: scratch of a layer of other sizes")
-        if scratch is not None and kept != "mx8":
+        if scratch is not None and held(kept, products) == "bf16":
             raise ShardConvError(4, "ShardedMLP: with kept=\"bf16\" the buffers are what the backward pass reads: not shared")
         self.device = torch.device(device)
         f32, bf16, dev = torch.float32, torch.bfloat16, self.device
