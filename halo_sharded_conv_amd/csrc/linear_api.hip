@@ -238,6 +238,9 @@ st_status st_linear(int64_t rows, int64_t in, int64_t out, const st_rows* x, con
                    meet(p.f.y, rows, out, p.f.pre, rows, out) || meet(p.f.pre, rows, out, p.f.res, rows, out) ||
                    (meet(p.f.y, rows, out, p.f.res, rows, out) && !same_rows(p.f.y, p.f.res))))
     return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": an output overlaps an input or the other output");
+  const Rows bv = floats_of(bias_or_null, out);
+  if (meet(p.f.y, rows, out, bv, 1, out) || meet(p.f.pre, rows, out, bv, 1, out))
+    return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": an output overlaps the bias");
   p.type = p.a.type;
   const Layout l = layout_of(rows, in, out, p.type, false);
   if (rows > 0 && l.total > 0 && (!workspace || workspace_bytes < l.total))
@@ -285,7 +288,11 @@ st_status st_linear_backward(int64_t rows, int64_t in, int64_t out, const st_row
   for (const Side& o : outs)
     for (const Side& i : ins)
       if (meet(*o.r, o.rows, o.cols, *i.r, i.rows, i.cols)) return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": an output overlaps an input");
-  if (meet(dx, rows, in, dw, out, in)) return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": two outputs overlap");
+  const Rows db = floats_of(dbias_or_null, out);
+  for (const Side& i : ins)
+    if (meet(db, 1, out, *i.r, i.rows, i.cols)) return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": dbias overlaps an input");
+  if (meet(dx, rows, in, dw, out, in) || meet(db, 1, out, dx, rows, in) || meet(db, 1, out, dw, out, in))
+    return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": two outputs overlap");
   const int type = rw.type, es = type_size(type);
   const Layout l = layout_of(rows, in, out, type, true);
   if (rows > 0 && (!workspace || workspace_bytes < l.total)) return fail(ST_ERR_WORKSPACE, std::string(me) + ": workspace missing or too small");

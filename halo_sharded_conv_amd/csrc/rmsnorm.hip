@@ -438,6 +438,12 @@ st_status st_rmsnorm(int64_t rows, int64_t channels, const st_rows* x, const st_
     for (int j = 0; j < i; ++j)
       if (rows_meet(*out[i], *out[j], rows, channels)) return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": two outputs overlap");
   }
+  const Rows gv = floats_of(gamma_or_null, channels), rv = floats_of(rstd_or_null, rows);
+  for (const Rows* r : {&a.total, &a.y, &a.y8})
+    if (meet(*r, rows, channels, gv, 1, channels)) return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": an output overlaps gamma");
+  for (const Rows* r : {&a.x, &a.res, &a.total, &a.y, &a.y8})
+    if (meet(*r, rows, channels, rv, 1, rows)) return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": rstd overlaps an operand");
+  if (rows > 0 && meet(gv, 1, channels, rv, 1, rows)) return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": rstd overlaps gamma");
   if (rows == 0) return ok();
   a.rows = (int32_t)rows;
   a.channels = (int32_t)channels;
@@ -493,6 +499,12 @@ st_status st_rmsnorm_backward(int64_t rows, int64_t channels, const st_rows* s_,
   if (rows_meet(a.y, a.x, rows, channels) || (rows_meet(a.y, a.total, rows, channels) && !same_rows(a.y, a.total)) ||
       (rows_meet(a.y, a.res, rows, channels) && !same_rows(a.y, a.res)))
     return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": dx overlaps an input");
+  const Rows gv = floats_of(gamma_or_null, channels), rv = floats_of(rstd, rows), dg = floats_of(dgamma_or_null, channels);
+  if (meet(a.y, rows, channels, gv, 1, channels) || meet(a.y, rows, channels, rv, 1, rows))
+    return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": dx overlaps gamma or rstd");
+  bool shared = meet(dg, 1, channels, gv, 1, channels) || (rows > 0 && meet(dg, 1, channels, rv, 1, rows));
+  for (const Rows* r : {&a.x, &a.total, &a.res, &a.y}) shared = shared || meet(*r, rows, channels, dg, 1, channels);
+  if (shared) return fail(ST_ERR_BAD_SHAPE, std::string(me) + ": dgamma overlaps an operand");
   if (dgamma_or_null && (!workspace || workspace_bytes < st_rmsnorm_backward_workspace_bytes(rows, channels)))
     return fail(ST_ERR_WORKSPACE, std::string(me) + ": workspace missing or too small");
   const hipStream_t st = static_cast<hipStream_t>(stream);

@@ -64,11 +64,13 @@ constexpr uint32_t kTakesFloat = 1u << ST_F32 | 1u << ST_BF16;
 constexpr uint32_t kTakesAll = kTakesFloat | 1u << ST_MX8;
 
 // True where two operands share bytes: `arows` rows of `ac` channels and `brows` of
-// `bc`.  Views of one buffer with one stride and columns apart do not.
+// `bc`.  Views of one buffer with one stride and columns apart do not, nor does one
+// row that lies between the rows of another operand.
 inline bool bytes_meet(const void* ap, int64_t as, int64_t an, int64_t arows, const void* bp, int64_t bs, int64_t bn, int64_t brows) {
   const char *a = static_cast<const char*>(ap), *b = static_cast<const char*>(bp);
   if (!(a < b + (brows - 1) * bs + bn && b < a + (arows - 1) * as + an)) return false;
-  if (arows > 1 && brows > 1 && as == bs) {
+  if (arows == 1 && brows > 1) return bytes_meet(bp, bs, bn, brows, ap, as, an, arows);
+  if (arows > 1 && (brows == 1 || as == bs)) {
     const int64_t d = ((b - a) % as + as) % as;             // b's rows start d bytes after a's
     return d < an || d + bn > as;
   }
@@ -83,6 +85,15 @@ inline bool meet(const Rows& a, int64_t arows, int64_t ac, const Rows& b, int64_
     for (int j = 0; j < 2; ++j)
       if (p[0][i] && p[1][j] && bytes_meet(p[0][i], s[0][i], n[0][i], arows, p[1][j], s[1][j], n[1][j], brows)) return true;
   return false;
+}
+// `n` floats beside the rows (a bias, a gamma, sums), as one row
+inline Rows floats_of(const float* p, int64_t n) {
+  Rows r = no_rows();
+  if (!p) return r;
+  r.p = reinterpret_cast<char*>(const_cast<float*>(p));
+  r.stride = 4 * n;
+  r.type = ST_F32;
+  return r;
 }
 inline bool rows_meet(const Rows& a, const Rows& b, int64_t rows, int64_t channels) { return meet(a, rows, channels, b, rows, channels); }
 // The same rows in the same type: what an operator that reads before it writes may take

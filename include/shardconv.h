@@ -827,8 +827,8 @@ st_status st_mx8_load(int64_t rows, int64_t channels, const st_rows* x, int32_t 
  *   dgamma_or_null  `channels` floats
  *   workspace       >= st_rmsnorm_backward_workspace_bytes(rows, channels) bytes
  * dgamma is summed in fp32 in an order fixed by the sizes and types (no atomics).
- * Errors of both: ST_ERR_INVALID_ARG, ST_ERR_BAD_SHAPE (outputs that overlap an
- * input or one another), ST_ERR_UNSUPPORTED (more than 16384 channels; 2^31 - 1024
+ * Errors of both: ST_ERR_INVALID_ARG, ST_ERR_BAD_SHAPE (outputs, rstd and dgamma among
+ * them, that overlap an input or one another), ST_ERR_UNSUPPORTED (more than 16384 channels; 2^31 - 1024
  * rows or more),
  * ST_ERR_WORKSPACE, ST_ERR_ALIGNMENT, ST_ERR_HIP.
  */
@@ -862,6 +862,7 @@ st_status st_rmsnorm_backward(int64_t rows, int64_t channels, const st_rows* s, 
  * cut the products of eight steps 13 bits below the largest.  Few rows stream the weights once; where tiles are few
  * the products' sum is split over workgroups and joined in a fixed order: the
  * bits depend on sizes and types only.
+ * y and pre must not overlap an input (bias among them; y may be residual, as above) or one another.
  * Errors: ST_ERR_WORKSPACE, ST_ERR_ALIGNMENT, ST_ERR_BAD_SHAPE, ST_ERR_UNSUPPORTED (larger
  * sizes, rows 4 MiB or more apart, more tiles than one launch holds), ST_ERR_INVALID_ARG,
  * ST_ERR_HIP.
@@ -880,9 +881,9 @@ st_status st_linear(int64_t rows, int64_t in, int64_t out, const st_rows* x, con
  *   w               fp32 or bf16; the products run in its type (p is rounded to it)
  *   pre_or_null     as the forward call wrote it, any type; NULL with ST_ACT_NONE only
  *   dy              fp32 or bf16
- *   dx_or_null, dw_or_null   fp32 or bf16, or NULL (not computed); must not
- *                   overlap an input
+ *   dx_or_null, dw_or_null   fp32 or bf16, or NULL (not computed)
  *   dbias_or_null   `out` floats (summed from fp32 p), or NULL
+ *                   (outputs must not overlap an input or one another)
  *   workspace       >= st_linear_workspace_bytes(rows, in, out, w's type, 1) bytes
  * rows == 0 clears dw and dbias.  No atomics: the bits depend on sizes and types
  * only.  Errors as st_linear.
