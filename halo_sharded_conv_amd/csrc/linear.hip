@@ -541,8 +541,9 @@ template <class T, bool AC, bool BC, bool PLAIN> st_status gemm_launch(const Gem
   if constexpr (std::is_same<T, MX8X>::value) gemm<T, AC, BC, 128, 64, 2, 2, 2, PLAIN><<<grid, 256, 0, st>>>(g);
   else if (shape == 2) gemm<T, AC, BC, 64, 64, 2, 2, 4, PLAIN><<<grid, 256, 0, st>>>(g);
   else if (shape == 1) gemm<T, AC, BC, 128, 64, 2, 2, std::is_same<T, MX8>::value ? 2 : 3, PLAIN><<<grid, 256, 0, st>>>(g);
-  else if constexpr (std::is_same<T, F32>::value) gemm<T, AC, BC, 128, 128, 2, 2, 2, PLAIN><<<grid, 256, 0, st>>>(g);
-  else gemm<T, AC, BC, 256, 256, 2, 4, 2, PLAIN><<<grid, 512, 0, st>>>(g);
+  else if constexpr (!std::is_same<T, F32>::value) gemm<T, AC, BC, 256, 256, 2, 4, 2, PLAIN><<<grid, 512, 0, st>>>(g);
+  else if constexpr (PLAIN) gemm<T, AC, BC, 128, 128, 2, 2, 2, true><<<grid, 256, 0, st>>>(g);
+  else return fail(ST_ERR_UNSUPPORTED, "matrix product: no such tile");   // (comes with split sums alone, which are plain)
   return launch_check("gemm");
 }
 

@@ -22,8 +22,13 @@ inline int stage_steps(int type) { return type == ST_F32 ? 32 : type == ST_BF16 
 struct Shape {                        // tile and what a compute unit holds of it
   int ta, tb, per_cu;
 };
-// large and small tile; fp32 (products a ninth as fast, twice the registers per
-// fragment) stays with 128 x 128
+// large, middle and small tile.  fp32 (products a ninth as fast, twice the registers per
+// fragment) has 128 x 128 for a large one, taken for long contractions alone and there
+// with split sums, never with whole ones: weight gradients of many rows (55053 rows,
+// 1818 to 1494 channels: 2655 us, with the smaller tiles 3010; 124716 rows, 4312 to
+// 1530: 13.5 ms, 14.7).
+// (8-bit operands: two of the 128 x 64 tiles fit a compute unit's LDS, not three; the
+// third of the workgroups start when others have ended.)
 constexpr Shape kShapes[2][3] = {{{256, 256, 1}, {128, 64, 3}, {64, 64, 4}}, {{128, 128, 2}, {128, 64, 3}, {64, 64, 4}}};
 inline const Shape& shape_of(int type, int s) { return kShapes[type == ST_F32][s]; }
 constexpr int kFewShape = 3;

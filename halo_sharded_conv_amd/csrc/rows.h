@@ -136,10 +136,6 @@ template <class T, int VEC> __device__ __forceinline__ void load_some(const char
     }
   }
 }
-template <int VEC> __device__ __forceinline__ void load_some(int type, const char* p, int n, float (&x)[VEC]) {
-  if (type == ST_F32) load_some<F32, VEC>(p, n, x);
-  else load_some<BF16, VEC>(p, n, x);
-}
 
 // A group as it lies in memory, unpacked when it is used: a load that is unpacked
 // where its type is looked at would be waited for there, one after the other.

@@ -2,6 +2,7 @@
 arithmetic of csrc/linear_plan.h, compiled for the host."""
 import ctypes
 import os
+import random
 import subprocess
 
 import pytest
@@ -83,3 +84,15 @@ def test_every_tile_has_its_sizes():
                          *((p, "f32", False, t) for p in ("y", "dx", "dw") for t in ((128, 128), (128, 64), (64, 64)))}
     for key, stages in seen.items():
         assert key[3] == (128, 128) or len(stages) >= 3, key
+
+
+def test_large_fp32_tiles_have_split_sums(plan):
+    """Which is why they need no other epilogue than the partial sums'."""
+    rng = random.Random(1)
+    size = lambda lo, hi: int(round(2 ** rng.uniform(lo, hi)))  # noqa: E731
+    large = 0
+    for _ in range(20000):
+        shape, splits = choose(plan, size(0, 20), size(0, 14), size(0, 20), "f32", cols=rng.random() < 0.5)[:2]
+        assert shape != 0 or splits > 1
+        large += shape == 0
+    assert large > 0
