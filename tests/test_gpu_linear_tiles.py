@@ -153,3 +153,20 @@ def test_eight_bit_outputs_are_the_fp32_outputs_rounded(gpu_lib, m, k, n, act):
         yo, po = run(y, pre)
         assert same(gpu_lib, yo, yf, y), f"y {y} pre {pre}"
         assert not pre or same(gpu_lib, po, zf, pre), f"pre {pre} y {y}"
+
+
+@pytest.mark.parametrize("m,k,n", [(7, 200, 96), (40, 8192, 260), (300, 9000, 260), (8449, 1000, 2304), (2716, 257, 2299)])
+@pytest.mark.parametrize("dtype", ["bf16", "mx8", "f32"])
+@pytest.mark.parametrize("stream", ["f32", "bf16"])
+def test_output_in_the_residuals_place(gpu_lib, m, k, n, dtype, stream):
+    """Few rows, split and joined sums, several tiles a workgroup: the bits of an output
+    of its own."""
+    say(f"linear {m}x{k}x{n} {dtype} onto its {stream} residual")
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    normal = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    x, w, r = held(gpu_lib, normal(m, k), dtype), held(gpu_lib, normal(n, k) / math.sqrt(k), dtype), normal(m, n).to(TORCH[stream])
+    ws = torch.empty(max(16, gpu_lib.st_linear_workspace_bytes(m, k, n, dtype)), dtype=torch.uint8, device="cuda")
+    apart = torch.empty_like(r)
+    gpu_lib.st_linear(x, w, None, apart, act="silu", residual=r, workspace=ws)
+    gpu_lib.st_linear(x, w, None, r, act="silu", residual=r, workspace=ws)
+    assert bool(torch.isfinite(apart).all()) and torch.equal(apart, r)
