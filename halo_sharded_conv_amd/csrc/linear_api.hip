@@ -6,6 +6,10 @@
 // keeps the sums of its own 8 columns over the rows it visits, a workgroup adds
 // its threads in a fixed order and writes one partial row, and a second kernel
 // adds those in order.  With no activation p is dy itself.
+//
+// p in bf16 is what the bf16 matrix cores take: half of 2^-8 of every term, independent
+// from term to term.  dx and dw of 16384 x 2048 x 8192 with GELU are 0.0023 of the norm off,
+// 0.0017 of it by their own rounding (an fp32 p: that alone, at a tenth of the rate).
 #include "linear.h"
 
 namespace st {

@@ -51,8 +51,10 @@ constexpr Pace kPace[2][3] = {{{1.0, 1.45, 7.0}, {0.48, 0.33, 3.0}, {0.42, 0.22,
 
 // Tile shape and split of the contraction: the least time of the fullest compute
 // unit, with the partial sums' way through memory (7 TB/s, 5 us for the join).
-// exact: 8-bit operands with an output that is no bf16, which the middle tile alone has.  cols:
-// the weights are read across their rows.
+// exact: 8-bit operands with an output that is no bf16, which the middle tile alone has:
+// its paces are the 8-bit instructions', of which the widened products take almost three
+// times as long (16384 x 2048 x 8192: 1076 us, by the paces 404).  cols: the weights are
+// read across their rows.
 inline Choice choose(int64_t m, int64_t n, int64_t k, int type, bool exact, bool cols) {
   const int kt = stage_steps(type);
   const int64_t stages = (k + kt - 1) / kt;

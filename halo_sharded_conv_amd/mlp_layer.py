@@ -18,9 +18,13 @@ one model may share (`scratch`).
 
 products="mx8" (forward only: nothing is kept, so that every buffer of the steps is
 scratch, whatever `kept` says) multiplies in 8 bits: weights rounded once, the norm's
-output where it is written, the hidden values in a pass of their own (from
-bf16: an 8-bit output of an 8-bit product would widen its operands, 128^2 cells of 2048 to
-8192 channels 1608 us, so 844).
+output where it is written, the hidden values in a pass of their own from
+bf16 (128^2 cells of 2048 to 8192 channels 844 us; an 8-bit output of the product itself
+would widen its operands, 1608).  So the hidden values are rounded twice, to bf16 from
+sums that the 8-bit instructions cut and then to 8 bits: 3.4% of the codes differ from
+those of one rounding, 0.017 of the norm, but the values are as near to the unrounded
+ones (2.66% of the norm off, once rounded 2.65%).  The output is bf16, so that the stream
+of several such layers is rounded to it in each.
 
 torch is used for allocation and views only.
 """

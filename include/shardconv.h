@@ -846,7 +846,8 @@ st_status st_rmsnorm_backward(int64_t rows, int64_t channels, const st_rows* s, 
 /*
  * st_linear - y = act(x w^T + bias) + residual in one pass over the products.
  *   rows, in, out     x is [rows][in], w [out][in], y [rows][out]; rows >= 0 and below
- *                     2^30, in and out >= 1 and below 2^24
+ *                     2^30, in and out >= 1 and below 2^24, a row of x and of w below 4 MiB
+ *                     (in the gradients of dy and pre too)
  *   x, w              one type: fp32, bf16, or both in the 8-bit form (inference)
  *   bias_or_null      `out` floats
  *   act               ST_ACT_*
@@ -859,9 +860,12 @@ st_status st_rmsnorm_backward(int64_t rows, int64_t channels, const st_rows* s, 
  * bf16 operands multiply on the matrix cores with fp32 accumulation, fp32 operands
  * in fp32.  8-bit operands do so too where y and pre are bf16; with another
  * output they are widened to bf16 (exactly) on the way, since the 8-bit instructions
- * cut the products of eight steps 13 bits below the largest.  Few rows stream the weights once; where tiles are few
- * the products' sum is split over workgroups and joined in a fixed order: the
- * bits depend on sizes and types only.
+ * cut the products of eight steps 13 bits below the largest; large products take
+ * four times as long then, longer than those of bf16 operands.  Few rows stream the
+ * weights once; where tiles are few the products' sum is split over workgroups and
+ * joined in a fixed order: the bits depend on sizes and types only.
+ * y and pre must not overlap an input, bias among them, or one another (y may be
+ * residual, as above).
  * y and pre must not overlap an input (bias among them; y may be residual, as above) or one another.
  * Errors: ST_ERR_WORKSPACE, ST_ERR_ALIGNMENT, ST_ERR_BAD_SHAPE, ST_ERR_UNSUPPORTED (larger
  * sizes, rows 4 MiB or more apart, more tiles than one launch holds), ST_ERR_INVALID_ARG,
