@@ -351,6 +351,19 @@ __device__ __forceinline__ void add_res(const Rows& o, int n0, int cols, Res& t,
   for (int r = 0; r < 16; ++r) v[r] += __uint_as_float(t.w[r / 4][r % 4]);
 }
 
+// The bias of a block's channels, from memory
+__device__ __forceinline__ void add_bias(const Finish& f, int n0, int lane, float (&v)[16]) {
+  if (!f.bias) return;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int n = n0 + 8 * q + 4 * (lane >> 5);
+    float t[4];
+    load_some<F32, 4>(reinterpret_cast<const char*>(f.bias + n), f.cols - n, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * q + i] += t[i];
+  }
+}
+
 // v = x w^T + bias: pre = v; y = act(v) + residual.  Every lane of the wave comes
 // here; `t`: the block of the residual, if there is one.
 // PLAIN: v alone, to bf16 or fp32.

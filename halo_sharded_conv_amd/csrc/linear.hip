@@ -84,7 +84,7 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
   __shared__ __attribute__((aligned(1024))) char b0[OB::BYTES];
   __shared__ __attribute__((aligned(1024))) char b1[OB::BYTES];
   __shared__ __attribute__((aligned(1024))) char sc[2 * SCALES];
-  __shared__ __attribute__((aligned(1024))) float bias[TA];
+  __shared__ __attribute__((aligned(1024))) float bias[2][TA];          // this tile's, the next one's
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, wa = wave % WA, wb = wave / WA;
   // (what depends on it is formed anew for each tile: no registers held meanwhile)
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
   const uint32_t xcd = blockIdx.x & 7, tiles = (uint32_t)g.tiles_a * g.tiles_b, total = tiles * g.splits;
   const uint32_t t_step = (gridDim.x + 7 - xcd) >> 3, t_end = (xcd + 1) * (total >> 3) + min(xcd + 1, total & 7);
   uint32_t t = xcd * (total >> 3) + min(xcd, total & 7) + (blockIdx.x >> 3);
-  int n0, m0, split, k_lo, k_hi;
+  int n0, m0, split, k_lo, k_hi, turn = 0;
   // this lane's transfers: byte offsets from a stage's base, of the first one where
   // the others are rows on
   constexpr int QA = OA::ALIKE ? 1 : OA::NI, QB = OB::ALIKE ? 1 : OB::NI;
@@ -164,10 +164,13 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
       }
     }
   };
-  // The tile's bias (the first split's; zeros past the last channel)
+  // The tile's bias (zeros past the last channel).  It is added to the whole sum, at the
+  // end: against a bias that the sums start from, the matrix instructions cut the
+  // products' lowest bits (5092 x 11 x 3264: 21 of the 8-bit codes on the other side in
+  // place of 2).
   auto fetch_bias = [&]() __attribute__((always_inline)) -> void {
     if (wave < TA / 64) {
-      to_lds<4, true>(g.f.bias, g.f.bias && split == 0 ? g.n * 4 : 0, bias + wave * 64, (uint32_t)(n0 + wave * 64 + lane_anew()) * 4, 0);
+      to_lds<4, true>(g.f.bias, g.f.bias ? g.n * 4 : 0, bias[turn] + wave * 64, (uint32_t)(n0 + wave * 64 + lane_anew()) * 4, 0);
     }
   };
 
@@ -282,18 +285,10 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
     else wait_vm<0>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    // the sums start from the bias
-    const int bias_at = wa * PA + (lane_anew() >> 5) * 4;
 #pragma unroll
-    for (int i = 0; i < NA; ++i) {
+    for (int i = 0; i < NA; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4 t = *reinterpret_cast<const float4*>(bias + bias_at + 32 * i + 8 * q);
-        acc[i][0][4 * q] = t.x; acc[i][0][4 * q + 1] = t.y; acc[i][0][4 * q + 2] = t.z; acc[i][0][4 * q + 3] = t.w;
-      }
-#pragma unroll
-      for (int j = 1; j < NB; ++j) acc[i][j] = acc[i][0];
-    }
+      for (int j = 0; j < NB; ++j) acc[i][j] = f32x16{};
     read_scales(Int<0>{}, k_lo);
     read(Int<0>{}, Int<0>{}, Int<0>{}, a0, b0);
     int kt = k_lo;
@@ -311,6 +306,8 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
     __builtin_amdgcn_s_waitcnt(0x0070);                 // (no transfer of this tile meets one of the next)
     asm volatile("" ::: "memory");
     const int em = m0 + wb * PB, en = n0 + wa * PA, es = split;
+    const float* ebias = bias[turn] + wa * PA;
+    turn ^= 1;                                          // (the other's readers were the epilogue before this one)
     const bool added = !PLAIN && g.f.res.type >= 0;
     constexpr bool AHEAD = !MX;                         // (8-bit operands: no registers for it)
     Res res[2];                                         // the block's, the next one's
@@ -350,6 +347,11 @@ __global__ __launch_bounds__(64 * WA * WB, OCC) void gemm(const GemmArgs g) {
             *reinterpret_cast<f32x4_t*>(p + 8 * q) = f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
         }
       } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 t = *reinterpret_cast<const float4*>(ebias + 32 * i + 8 * q + 4 * (l >> 5));
+          v[4 * q] += t.x; v[4 * q + 1] += t.y; v[4 * q + 2] += t.z; v[4 * q + 3] += t.w;
+        }
         finish_block<PLAIN, TA == 256>(g.f, m, n, l, res[AHEAD ? u & 1 : 0], v);
       }
     });
@@ -393,6 +395,7 @@ __global__ __launch_bounds__(64) void gemm_join(const float* __restrict__ part, 
       for (int r = 0; r < 16; ++r) v[r] += t[r / 4][r % 4];
     }
   }
+  add_bias(f, n0, lane, v);
   finish_block<false>(f, m0, n0, lane, t, v);
 }
 
@@ -496,18 +499,9 @@ template <class T, int MB> __global__ __launch_bounds__(64 * kFewWaves, 2) void 
     v[4 * q] = t.x; v[4 * q + 1] = t.y; v[4 * q + 2] = t.z; v[4 * q + 3] = t.w;
   }
   const int64_t m = 32 * wave + l32;
-  if (g.f.bias && split == 0) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = n0 + 8 * q + 4 * half;
-      float t[4];
-      load_some<F32, 4>(reinterpret_cast<const char*>(g.f.bias + n), g.n - n, t);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * q + i] += t[i];
-    }
-  }
   if (!g.part) {
     Res t;
+    add_bias(g.f, n0, lane, v);
     if (g.f.res.type >= 0) load_res(g.f.res, 32 * wave, n0, g.f.rows, g.f.cols, lane, t);
     finish_block<false>(g.f, 32 * wave, n0, lane, t, v);
   } else if (m < g.m) {
